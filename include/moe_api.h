@@ -393,6 +393,148 @@ MOE_API unsigned long long moe_set_grid_wait_budget_ns(unsigned long long ns);
  */
 MOE_API int moe_read_device_status(void* workspace, void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * Routing rules with expert groups, and the layer in 8-bit integers.
+ */
+
+/*
+ * How experts are chosen from router logits r [E]:
+ *   s_e   = softmax(r)_e or sigma(r_e)             (score_mode, MOE_SCORE_*)
+ *   key_e = s_e + select_bias_e                    (select_bias NULL: key_e = s_e)
+ *   the experts form n_group groups of E / n_group neighbours; a group's score is the sum of
+ *   its group_top (1 or 2) largest keys, and only the topk_group groups of largest score stay
+ *   I     = TopK(key, K) inside those groups, by descending key, ties to the lower index
+ *   w_e   = scale * s_e / (renorm ? sum_{j in I} s_j : 1)
+ * The order is that of the real numbers key_e: fp32 values that are too close to tell are
+ * compared again in fp64.  A logit of -inf or NaN takes its expert out for that token (so
+ * does a bias of -inf or NaN for all tokens): it adds to no group score, is chosen only when
+ * fewer than K others are left, and has weight 0.  A logit of +inf counts as the largest
+ * finite number.  n_group <= 32 divides E, 1 <= topk_group <= n_group, and
+ * topk_group * (E / n_group) >= K; MOE_ERR_ARG otherwise (MOE_ERR_UNSUPPORTED for n_group > 32).
+ */
+typedef struct moe_route_rule {
+    int score_mode;
+    const float* select_bias; /* [E] device, or NULL */
+    int n_group, topk_group;  /* 1, 1: no groups */
+    int group_top;            /* 1 or 2 */
+    int renorm;               /* 0: weights are scale * s_e */
+    float scale;              /* finite; 1 for none */
+} moe_route_rule;
+
+#define MOE_DTYPE_F32 0
+#define MOE_DTYPE_BF16 1
+
+/*
+ * Routing from given logits (device, [T, E] row-major contiguous, MOE_DTYPE_*): topk_idx
+ * [T, K] int32, topk_w [T, K] fp32 and expert_counts [E] int32 (overwritten; or NULL) as
+ * moe_route, by `rule`.  1 <= E <= 512, 1 <= K <= min(E, 16).  No workspace.
+ */
+MOE_API int moe_route_logits(const void* logits, int logits_dtype, int T, int E, int K,
+                             const moe_route_rule* rule, int32_t* topk_idx, float* topk_w,
+                             int32_t* expert_counts, void* stream);
+
+/*
+ * moe_route_ex with a rule: the logits x W_r^T + logit_bias (fp32 accumulate) as moe_route,
+ * the selection and weights by `rule`.  Other arguments, outputs and errors as moe_route.
+ */
+MOE_API int moe_route_rule_ex(const moe_bf16* x, const moe_bf16* w_router, const float* logit_bias,
+                              const moe_bf16* w_shared_gate, int T, int D, int E, int K,
+                              const moe_route_rule* rule, int32_t* topk_idx, float* topk_w,
+                              int32_t* expert_counts, float* shared_gate, void* workspace,
+                              size_t ws_bytes, void* stream);
+
+/*
+ * Rows to 8-bit integers, one scale per row (tokens of an activation, output channels of a
+ * weight): scale_r = max_c |x[r, c]| / 127, q[r, c] = rint(127 x[r, c] / max_c |x[r, c]|) to
+ * nearest even, exactly; |q| <= 127.  A zero row has scale 0 and q 0; a row that holds a NaN or
+ * an infinity has scale NaN and q 0, so that what is computed from it is NaN.
+ *   x [rows, cols] bf16, q [rows, cols] int8, scale [rows] fp32; cols a multiple of 16
+ */
+MOE_API int moe_quantize_rows(const moe_bf16* x, long long rows, int cols, int8_t* q, float* scale,
+                              void* stream);
+
+/*
+ * Product of 8-bit integers with a scale for each token and each output channel:
+ *   out[t, n] = bf16( x_scale[t] * w_scale[n] * sum_k xq[t, k] wq[n, k] )
+ *   xq [T, K] int8, x_scale [T], wq [N, K] int8 row-major, w_scale [N], out [T, N] bf16
+ * The sum is an exact int32 (any int8 values).  K a multiple of 16 up to 65536, N a
+ * multiple of 8 up to 2^20.  w_scale 16-byte aligned like the matrices.
+ * workspace: moe_int8_workspace_size(T, N, K) bytes, 256-byte aligned; no initialisation.
+ */
+MOE_API size_t moe_int8_workspace_size(int T, int N, int K);
+MOE_API int moe_int8_matmul(const int8_t* xq, const float* x_scale, const int8_t* wq,
+                            const float* w_scale, int T, int N, int K, moe_bf16* out,
+                            void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * A linear layer in 8-bit integers: moe_quantize_rows of x [T, K] bf16, then
+ * moe_int8_matmul.  Same limits and workspace.
+ */
+MOE_API int moe_int8_linear(const moe_bf16* x, const int8_t* wq, const float* w_scale, int T, int N,
+                            int K, moe_bf16* out, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * The routed SwiGLU experts in 8-bit integers, for a routing and permutation in hand
+ * (moe_permute): for row r of expert e with token t = sorted_token[r]
+ *   h_r = SiLU(W_gate^e x_t) (.) (W_up^e x_t)    int32 sums, scaled, fp32
+ *   h_r is quantised again as moe_quantize_rows does
+ *   out[t, :] = bf16( residual[t, :] + sum over t's rows of sorted_w[r] * W_down^e h_r )
+ * with W^e = scale[n] * wq[n, :] for weight row n.  Rows from expert_offsets[E] on are left
+ * out (a capacity dropped them); a token without rows gets its residual (or 0).
+ * No kernel waits for another CTA's work, so calls with workspaces of their own may run on
+ * several streams at once.
+ */
+typedef struct moe_int8_experts {
+    const int8_t* xq;               /* [T, D] */
+    const float* x_scale;           /* [T] */
+    const int32_t* expert_offsets;  /* [E+1] */
+    const int32_t* sorted_token;    /* [T*K] */
+    const float* sorted_w;          /* [T*K] */
+    const int32_t* slot_to_row;     /* [T*K] */
+    const float* topk_w;            /* [T, K]; read with MOE_FLAG_DETERMINISTIC only */
+    const int8_t* w_gate_up;        /* [E, 2f, D] */
+    const float* gate_up_scale;     /* [E, 2f] */
+    const int8_t* w_down;           /* [E, D, f] */
+    const float* down_scale;        /* [E, D] */
+    const moe_bf16* residual;       /* [T, D], or NULL */
+    int T, D, E, K, f;              /* as moe_layer_forward */
+    unsigned flags;                 /* MOE_FLAG_DETERMINISTIC: fixed-order sums */
+} moe_int8_experts;
+
+/* Bytes of workspace for moe_experts_int8 (0: unsupported shape); 256-byte aligned. */
+MOE_API size_t moe_experts_int8_workspace_size(int T, int D, int E, int K, int f, unsigned flags);
+MOE_API int moe_experts_int8(const moe_int8_experts* p, moe_bf16* out, void* workspace,
+                             size_t ws_bytes, void* stream);
+
+/* The 8-bit weights of a layer (channel scales as in moe_int8_experts). */
+typedef struct moe_int8_weights {
+    const int8_t* gate_up;
+    const float* gate_up_scale;
+    const int8_t* down;
+    const float* down_scale;
+    const int8_t* shared_gate_up; /* [2 f_s, D], or NULL with f_s = 0 */
+    const float* shared_gate_up_scale;
+    const int8_t* shared_down;    /* [D, f_s] */
+    const float* shared_down_scale;
+} moe_int8_weights;
+
+/*
+ * moe_layer_forward with a routing rule and / or 8-bit weights.
+ *   rule     NULL: the routing of p (score_mode, select_bias); otherwise the rule's, and
+ *            p->score_mode / select_bias must be 0 / NULL and MOE_FLAG_BF16_WEIGHTS clear
+ *   weights  NULL: the bf16 weights of p; otherwise these, and p's w_gate_up, w_down,
+ *            w_shared_gate_up and w_shared_down must be NULL.  The router and the shared gate stay
+ *            bf16; the tokens are quantised once for the routed and the shared expert;
+ *            p->step_events must be NULL.
+ * workspace: moe_layer_ex_workspace_size bytes (int8: whether weights is given), 256-byte
+ * aligned.  Everything else as moe_layer_forward.
+ */
+MOE_API size_t moe_layer_ex_workspace_size(int T, int D, int E, int K, int f, int f_s, unsigned flags,
+                                           int int8);
+MOE_API int moe_layer_forward_ex(const moe_layer_params* p, const moe_route_rule* rule,
+                                 const moe_int8_weights* weights, moe_bf16* out, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

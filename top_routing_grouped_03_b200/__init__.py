@@ -9,6 +9,7 @@ machine without a CUDA device) the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -45,6 +46,30 @@ class LayerParams(ctypes.Structure):
         ("residual", ctypes.c_void_p),
         ("capacity_factor", ctypes.c_float), ("min_capacity", ctypes.c_int),
     ]
+
+
+class RouteRule(ctypes.Structure):
+    """moe_route_rule."""
+    _fields_ = [
+        ("score_mode", ctypes.c_int), ("select_bias", ctypes.c_void_p),
+        ("n_group", ctypes.c_int), ("topk_group", ctypes.c_int), ("group_top", ctypes.c_int),
+        ("renorm", ctypes.c_int), ("scale", ctypes.c_float),
+    ]
+
+
+class Int8Experts(ctypes.Structure):
+    """moe_int8_experts."""
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "xq", "x_scale", "expert_offsets", "sorted_token", "sorted_w", "slot_to_row", "topk_w",
+        "w_gate_up", "gate_up_scale", "w_down", "down_scale", "residual")] + \
+        [(n, ctypes.c_int) for n in ("T", "D", "E", "K", "f")] + [("flags", ctypes.c_uint)]
+
+
+class Int8Weights(ctypes.Structure):
+    """moe_int8_weights."""
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "gate_up", "gate_up_scale", "down", "down_scale", "shared_gate_up", "shared_gate_up_scale",
+        "shared_down", "shared_down_scale")]
 
 
 # Step boundaries recorded by moe_layer_forward when step_events is given.
@@ -101,6 +126,28 @@ def lib() -> ctypes.CDLL:
         L.moe_layer_plan.restype = I
         L.moe_set_grid_wait_budget_ns.argtypes = [ctypes.c_ulonglong]
         L.moe_set_grid_wait_budget_ns.restype = ctypes.c_ulonglong
+        RP = ctypes.POINTER(RouteRule)
+        L.moe_route_logits.argtypes = [P, I, I, I, I, RP, P, P, P, P]
+        L.moe_route_logits.restype = I
+        L.moe_route_rule_ex.argtypes = [P, P, P, P, I, I, I, I, RP, P, P, P, P, P, Z, P]
+        L.moe_route_rule_ex.restype = I
+        L.moe_quantize_rows.argtypes = [P, ctypes.c_longlong, I, P, P, P]
+        L.moe_quantize_rows.restype = I
+        L.moe_int8_workspace_size.argtypes = [I, I, I]
+        L.moe_int8_workspace_size.restype = Z
+        L.moe_int8_matmul.argtypes = [P, P, P, P, I, I, I, P, P, Z, P]
+        L.moe_int8_matmul.restype = I
+        L.moe_int8_linear.argtypes = [P, P, P, I, I, I, P, P, Z, P]
+        L.moe_int8_linear.restype = I
+        L.moe_experts_int8_workspace_size.argtypes = [I, I, I, I, I, ctypes.c_uint]
+        L.moe_experts_int8_workspace_size.restype = Z
+        L.moe_experts_int8.argtypes = [ctypes.POINTER(Int8Experts), P, P, Z, P]
+        L.moe_experts_int8.restype = I
+        L.moe_layer_ex_workspace_size.argtypes = [I, I, I, I, I, I, ctypes.c_uint, I]
+        L.moe_layer_ex_workspace_size.restype = Z
+        L.moe_layer_forward_ex.argtypes = [ctypes.POINTER(LayerParams), RP,
+                                           ctypes.POINTER(Int8Weights), P, P, Z, P]
+        L.moe_layer_forward_ex.restype = I
         _lib = L
     return _lib
 
@@ -118,7 +165,7 @@ def _check(rc: int, what: str):
         raise MoEError(rc, what)
 
 
-BF16, F32, I32, U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+BF16, F32, I32, U8, I8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.int8
 
 
 def _p(t: Optional[torch.Tensor], dtype: Optional[torch.dtype] = None):
@@ -154,10 +201,11 @@ def alloc_workspace(T, D, E, K, f, f_s=0, device=None) -> torch.Tensor:
 
 
 def route(x, w_router, K, logit_bias=None, w_shared_gate=None, workspace=None, stream=None,
-          score="softmax", select_bias=None, bf16_weights=False):
+          score="softmax", select_bias=None, bf16_weights=False, rule=None):
     """Router step.  Returns (topk_idx [T,K] int32, topk_w [T,K] f32, expert_counts [E]
     int32, shared_gate [T] f32 or None).  score / select_bias / bf16_weights select the
-    router variants of moe_route_ex."""
+    router variants of moe_route_ex; ``rule`` (a route_rule(...)) those of moe_route_rule_ex
+    instead."""
     T, D = x.shape
     E = w_router.shape[0]
     dev = x.device
@@ -166,7 +214,13 @@ def route(x, w_router, K, logit_bias=None, w_shared_gate=None, workspace=None, s
     w = torch.empty((T, K), dtype=torch.float32, device=dev)
     counts = torch.empty((E,), dtype=torch.int32, device=dev)
     sg = torch.empty((T,), dtype=torch.float32, device=dev) if w_shared_gate is not None else None
-    if score == "softmax" and select_bias is None and not bf16_weights:
+    if rule is not None:
+        _need(score == "softmax" and select_bias is None and not bf16_weights,
+              "route (a rule replaces score, select_bias and bf16_weights)")
+        rc = lib().moe_route_rule_ex(_p(x, BF16), _p(w_router, BF16), _p(logit_bias, F32),
+                                     _p(w_shared_gate, BF16), T, D, E, K, rule, _p(idx), _p(w),
+                                     _p(counts), _p(sg), _p(ws, U8), ws.numel(), _stream(stream))
+    elif score == "softmax" and select_bias is None and not bf16_weights:
         rc = lib().moe_route(_p(x, BF16), _p(w_router, BF16), _p(logit_bias, F32),
                              _p(w_shared_gate, BF16), T, D, E, K, _p(idx), _p(w), _p(counts),
                              _p(sg), _p(ws, U8), ws.numel(), _stream(stream))
@@ -249,6 +303,168 @@ def combine(T, D, K, out=None, out_acc=None, y_sorted=None, slot_to_row=None, to
     return out
 
 
+def _need(ok: bool, what: str):
+    if not ok:
+        raise MoEError(-1, what)
+
+
+def _on_device_of(fn):
+    """Runs fn with its first argument's device current and its ``stream`` (default: that
+    device's current stream) as the current one, so that what fn allocates belongs to it."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        if not first.is_cuda:
+            raise ValueError("expected a CUDA tensor")
+        dev = first.device
+        if stream is None and dev.index == torch.cuda.current_device():
+            return fn(first, *args, **kw)
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        if stream.device != dev:
+            raise ValueError(f"stream on {stream.device}, tensors on {dev}")
+        with torch.cuda.stream(stream):
+            return fn(first, *args, **kw)
+    return call
+
+
+def _q(t, dtype, dev):
+    """_p for a tensor that has to live on ``dev``."""
+    if t is not None and t.device != dev:
+        raise ValueError(f"expected a tensor on {dev}, got one on {t.device}")
+    return _p(t, dtype)
+
+
+def route_rule(E, K, score="softmax", select_bias=None, n_group=1, topk_group=1, group_top=None,
+               renorm=True, scale=1.0, device=None) -> RouteRule:
+    """A moe_route_rule.  group_top defaults to 2 with a select_bias (a group is judged by its two
+    best keys) and 1 without."""
+    if select_bias is not None:
+        _need(select_bias.shape == (E,), "route_rule (select_bias must be [E])")
+    if group_top is None:
+        group_top = 1 if select_bias is None else 2
+    bias = _p(select_bias, F32) if device is None else _q(select_bias, F32, device)
+    rule = RouteRule(SCORES[score], bias, n_group, topk_group, group_top, 1 if renorm else 0, scale)
+    rule.keep = select_bias  # the rule holds a bare pointer to it
+    return rule
+
+
+@_on_device_of
+def route_logits(logits, K, score="softmax", select_bias=None, n_group=1, topk_group=1,
+                 group_top=None, renorm=True, scale=1.0):
+    """Routing from given logits [T, E] (fp32 or bf16) by moe_route_logits: scores, a
+    selection-only bias, the topk_group best of n_group expert groups, TopK, weights
+    (renormalised, times scale).  Returns (topk_idx [T,K] int32, topk_w [T,K] f32,
+    expert_counts [E] int32)."""
+    _need(logits.dim() == 2, "route_logits (logits must be [T, E])")
+    T, E = logits.shape
+    dev = logits.device
+    if logits.dtype is not F32 and logits.dtype is not BF16:
+        raise TypeError(f"expected fp32 or bf16 logits, got {logits.dtype}")
+    rule = route_rule(E, K, score, select_bias, n_group, topk_group, group_top, renorm, scale, dev)
+    idx = torch.empty((T, K), dtype=I32, device=dev)
+    w = torch.empty((T, K), dtype=F32, device=dev)
+    counts = torch.empty((E,), dtype=I32, device=dev)
+    _check(lib().moe_route_logits(_p(logits), 0 if logits.dtype is F32 else 1, T, E, K, rule,
+                                  idx.data_ptr(), w.data_ptr(), counts.data_ptr(), _stream()),
+           "moe_route_logits")
+    return idx, w, counts
+
+
+@_on_device_of
+def quantize_rows(x):
+    """Rows of x [..., C] bf16 as 8-bit integers: (q int8 like x, scale [...] f32) with
+    x ~ q * scale (moe_quantize_rows)."""
+    _need(x.dim() >= 1, "quantize_rows (x must have rows)")
+    C = x.shape[-1]
+    q = torch.empty(x.shape, dtype=I8, device=x.device)
+    scale = torch.empty(x.shape[:-1], dtype=F32, device=x.device)
+    _check(lib().moe_quantize_rows(_p(x, BF16), scale.numel(), C, q.data_ptr(), scale.data_ptr(),
+                                   _stream()), "moe_quantize_rows")
+    return q, scale
+
+
+def _int8_workspace(T, N, K, dev, workspace):
+    n = int(lib().moe_int8_workspace_size(T, N, K))
+    if n == 0:
+        raise MoEError(-2, "moe_int8_workspace_size")
+    if workspace is None:
+        return torch.empty(n, dtype=U8, device=dev)
+    return workspace
+
+
+@_on_device_of
+def int8_matmul(xq, x_scale, wq, w_scale, workspace=None, out=None):
+    """out [T, N] bf16 = (xq wq^T) * x_scale[:, None] * w_scale[None, :] with xq [T, K] and
+    wq [N, K] int8 (moe_int8_matmul)."""
+    _need(xq.dim() == 2 and wq.dim() == 2 and xq.shape[1] == wq.shape[1],
+          "int8_matmul (xq must be [T, K], wq [N, K])")
+    (T, K), N, dev = xq.shape, wq.shape[0], xq.device
+    _need(x_scale.shape == (T,) and w_scale.shape == (N,), "int8_matmul (one scale per row)")
+    out = torch.empty((T, N), dtype=BF16, device=dev) if out is None else out
+    _need(out.shape == (T, N), "int8_matmul (out must be [T, N])")
+    ws = _int8_workspace(T, N, K, dev, workspace)
+    _check(lib().moe_int8_matmul(_p(xq, I8), _q(x_scale, F32, dev), _q(wq, I8, dev),
+                                 _q(w_scale, F32, dev), T, N, K, _q(out, BF16, dev),
+                                 _q(ws, U8, dev), ws.numel(), _stream()), "moe_int8_matmul")
+    return out
+
+
+@_on_device_of
+def int8_linear(x, wq, w_scale, workspace=None, out=None):
+    """A linear layer in 8-bit integers: x [T, K] bf16 quantised per row, times wq [N, K] int8
+    with w_scale [N]; returns [T, N] bf16 (moe_int8_linear)."""
+    _need(x.dim() == 2 and wq.dim() == 2 and x.shape[1] == wq.shape[1],
+          "int8_linear (x must be [T, K], wq [N, K])")
+    (T, K), N, dev = x.shape, wq.shape[0], x.device
+    _need(w_scale.shape == (N,), "int8_linear (one scale per weight row)")
+    out = torch.empty((T, N), dtype=BF16, device=dev) if out is None else out
+    _need(out.shape == (T, N), "int8_linear (out must be [T, N])")
+    ws = _int8_workspace(T, N, K, dev, workspace)
+    _check(lib().moe_int8_linear(_p(x, BF16), _q(wq, I8, dev), _q(w_scale, F32, dev), T, N, K,
+                                 _q(out, BF16, dev), _q(ws, U8, dev), ws.numel(), _stream()),
+           "moe_int8_linear")
+    return out
+
+
+@_on_device_of
+def experts_int8(xq, x_scale, topk_w, perm, w_gate_up, gate_up_scale, w_down, down_scale,
+                 residual=None, deterministic=False, workspace=None, out=None):
+    """The routed SwiGLU experts in 8-bit integers (moe_experts_int8): tokens xq [T, D] int8 with
+    x_scale [T] (quantize_rows), weights w_gate_up [E, 2f, D] and w_down [E, D, f] int8 with
+    gate_up_scale [E, 2f] and down_scale [E, D], for the routing weights topk_w [T, K] and
+    ``perm`` = permute(...).  Returns out [T, D] bf16 (+ residual).  Rows of ``perm`` are trusted:
+    they must index the T tokens and the E experts."""
+    _need(xq.dim() == 2 and w_gate_up.dim() == 3 and w_down.dim() == 3 and topk_w.dim() == 2,
+          "experts_int8 (xq [T, D], topk_w [T, K], w_gate_up [E, 2f, D], w_down [E, D, f])")
+    T, D = xq.shape
+    E, _, f = w_down.shape
+    K, dev = topk_w.shape[1], xq.device
+    _need(topk_w.shape[0] == T and w_down.shape[1] == D and w_gate_up.shape == (E, 2 * f, D),
+          "experts_int8 (weights and tokens of different shapes)")
+    _need(x_scale.shape == (T,) and gate_up_scale.shape == (E, 2 * f)
+          and down_scale.shape == (E, D), "experts_int8 (one scale per row)")
+    _need(perm["offsets"].numel() == E + 1 and perm["sorted_token"].numel() == T * K
+          and perm["sorted_w"].numel() == T * K and perm["slot_to_row"].numel() == T * K,
+          "experts_int8 (perm of another routing)")
+    out = torch.empty((T, D), dtype=BF16, device=dev) if out is None else out
+    _need(out.shape == (T, D) and (residual is None or residual.shape == (T, D)),
+          "experts_int8 (out and residual must be [T, D])")
+    flags = MOE_FLAG_DETERMINISTIC if deterministic else 0
+    if workspace is None:
+        n = int(lib().moe_experts_int8_workspace_size(T, D, E, K, f, flags))
+        if n == 0:
+            raise MoEError(-2, "moe_experts_int8_workspace_size")
+        workspace = torch.empty(n, dtype=U8, device=dev)
+    prm = Int8Experts(_p(xq, I8), _q(x_scale, F32, dev), _q(perm["offsets"], I32, dev),
+                      _q(perm["sorted_token"], I32, dev), _q(perm["sorted_w"], F32, dev),
+                      _q(perm["slot_to_row"], I32, dev), _q(topk_w, F32, dev),
+                      _q(w_gate_up, I8, dev), _q(gate_up_scale, F32, dev), _q(w_down, I8, dev),
+                      _q(down_scale, F32, dev), _q(residual, BF16, dev), T, D, E, K, f, flags)
+    _check(lib().moe_experts_int8(prm, _q(out, BF16, dev), _q(workspace, U8, dev),
+                                  workspace.numel(), _stream()), "moe_experts_int8")
+    return out
+
+
 def ep_dispatch_rows(x, sorted_token, rows, stream=None):
     """x_sorted [rows, D] bf16 = x[sorted_token[:rows]] (moe_ep_dispatch_rows)."""
     out = torch.empty((rows, x.shape[1]), dtype=BF16, device=x.device)
@@ -315,7 +531,7 @@ class MoELayer:
     def __init__(self, w_router, w_gate_up, w_down, K, logit_bias=None, w_shared_gate=None,
                  w_shared_gate_up=None, w_shared_down=None, deterministic=False,
                  score="softmax", select_bias=None, bf16_weights=False, capacity_factor=0.0,
-                 min_capacity=0):
+                 min_capacity=0, rule=None):
         self.w_router, self.w_gate_up, self.w_down = w_router, w_gate_up, w_down
         self.logit_bias = logit_bias
         self.w_shared_gate, self.w_shared_gate_up = w_shared_gate, w_shared_gate_up
@@ -330,6 +546,8 @@ class MoELayer:
         self.select_bias = select_bias
         self.capacity_factor = float(capacity_factor)
         self.min_capacity = int(min_capacity)
+        self.rule = rule  # a route_rule(...) instead of score / select_bias / bf16_weights
+        self._int8 = None
         self._ws = None
         self._ws_T = -1
         self._copy_streams = None
@@ -370,8 +588,12 @@ class MoELayer:
                                                       device=x.device)
         ws = self.workspace(T)
         prm = self.params(x, topk_idx, topk_w, counts, step_events, residual)
-        rc = lib().moe_layer_forward(ctypes.byref(prm), _p(out, BF16), _p(ws, U8), ws.numel(),
-                                     _stream(stream))
+        if self.rule is None and self._int8 is None:
+            rc = lib().moe_layer_forward(ctypes.byref(prm), _p(out, BF16), _p(ws, U8), ws.numel(),
+                                         _stream(stream))
+        else:
+            rc = lib().moe_layer_forward_ex(ctypes.byref(prm), self.rule, self._int8,
+                                            _p(out, BF16), _p(ws, U8), ws.numel(), _stream(stream))
         _check(rc, "moe_layer_forward")
         return out
 
@@ -439,3 +661,36 @@ class MoELayer:
 
     def device_status(self, stream=None) -> int:
         return read_device_status(self._ws, stream) if self._ws is not None else 0
+
+
+class Int8MoELayer(MoELayer):
+    """One MoE layer whose experts (and shared expert) are 8-bit integers.
+
+    Made from the bf16 weights of a MoELayer, which are quantised per output channel on
+    construction and not kept; the router and the shared gate stay bf16.  Same options and
+    calls as MoELayer, without step_events and plan()."""
+
+    def __init__(self, w_router, w_gate_up, w_down, K, logit_bias=None, w_shared_gate=None,
+                 w_shared_gate_up=None, w_shared_down=None, deterministic=False, **options):
+        super().__init__(w_router, w_gate_up, w_down, K, logit_bias, w_shared_gate,
+                         w_shared_gate_up, w_shared_down, deterministic, **options)
+        self.quantized = [None if w is None else quantize_rows(w)
+                          for w in (w_gate_up, w_down, w_shared_gate_up, w_shared_down)]
+        self.w_gate_up = self.w_down = self.w_shared_gate_up = self.w_shared_down = None
+        ptrs = []
+        for qs in self.quantized:
+            ptrs += [None, None] if qs is None else [_p(qs[0], I8), _p(qs[1], F32)]
+        self._int8 = Int8Weights(*ptrs)
+
+    def workspace(self, T: int) -> torch.Tensor:
+        n = int(lib().moe_layer_ex_workspace_size(T, self.D, self.E, self.K, self.f, self.f_s,
+                                                  self.flags, 1))
+        if n == 0:
+            raise MoEError(-2, "moe_layer_ex_workspace_size")
+        if self._ws is None or self._ws.numel() < n:
+            self._ws = torch.empty(n, dtype=U8, device=self.w_router.device)
+            self._ws[:256].zero_()
+        return self._ws
+
+    def plan(self, T: int):
+        raise MoEError(-2, "moe_layer_plan (a layer in 8-bit integers)")

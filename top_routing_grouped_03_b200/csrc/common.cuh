@@ -1,6 +1,7 @@
 // common.cuh -- types and small helpers shared by the kernels of libmoe_b200.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -117,6 +118,10 @@ struct RouterLaunch {
     const float* select_bias; // [E] added to the scores for the selection only, or NULL
     int bf16_weights;         // round the renormalised weights to bf16
     int logit_planes;         // tensor-core path: partial-sum planes of [T, E] in logits
+    // when not NULL, the logits go through launch_route_logits with this rule's scores,
+    // groups and weights instead of the selection above (topk_idx, topk_w, counts as given
+    // there); the shared gate is then computed by a kernel of its own
+    const struct RouteLogitsLaunch* rule;
 };
 cudaError_t launch_router(const RouterLaunch& a, int num_sms, cudaStream_t s, bool pdl = false);
 
@@ -129,8 +134,32 @@ bool router_uses_tensor_cores(int T, int E);
 int router_tc_max_planes(int T);
 cudaError_t launch_router_tc(const RouterLaunch& a, int num_sms, cudaStream_t s, bool pdl = false);
 
+// Routing from given logits (route_logits.cu).
+struct RouteLogitsLaunch {
+    const void* logits;       // [T, E] fp32 or bf16, rows row_stride elements apart
+    bool is_bf16;
+    long long row_stride;
+    int planes;               // partial sums of the logits, plane_stride elements apart, added in order
+    long long plane_stride;
+    const float* logit_bias;  // [E] added to the logits, or NULL
+    int T, E, K;
+    int score_mode;
+    const float* select_bias;
+    int n_group, topk_group, group_top;
+    int renorm;
+    float scale;
+    int32_t* topk_idx;
+    float* topk_w;
+    int32_t* counts;          // [E] overwritten, or NULL
+    // filled in by the launcher
+    int group_lanes, group_magic;
+};
+cudaError_t launch_route_logits(const RouteLogitsLaunch& a, int num_sms, cudaStream_t s,
+                                bool pdl = false);
 
-
+// moe_layer_forward with the routing of `rule` (NULL: of p).
+int layer_forward(const moe_layer_params* p, const RouteLogitsLaunch* rule, moe_bf16* out,
+                  void* workspace, size_t ws_bytes, void* stream);
 
 struct GroupedGemmLaunch {
     bool gate_up;               // true: SiLU(gate)*up epilogue -> h; false: down epilogue
@@ -186,6 +215,57 @@ cudaError_t launch_gather_rows(const bf16* x, const int32_t* tok, int rows, int 
                                int num_sms, cudaStream_t s, bool pdl);
 cudaError_t launch_grouped_gemm(const GroupedGemmLaunch& a, int num_sms, cudaStream_t s,
                                 bool pdl = false);
+
+// 2-D tensor map over `rows` rows of `cols` 2-byte elements (see grouped_gemm.cu), not cached
+cudaError_t encode_tile_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
+                            int box_rows);
+
+// ---------------------------------------------------------------- 8-bit integer operators
+
+// q[r, c] = rint(127 x[r, c] / amax_r), scale[r] = amax_r / 127 (quantize.cu).  A row with a NaN or an
+// infinity gets scale NaN and q = 0.  row_count (device, or NULL): rows past *row_count are
+// left alone.  clear (or NULL): clear_words 4-byte words set to 0 on the way.
+struct QuantizeLaunch {
+    const void* x;       // [rows, cols] bf16, or fp32 when is_f32
+    bool is_f32;
+    long long rows;
+    int cols;            // a multiple of 16
+    int8_t* q;
+    float* scale;
+    const int32_t* row_count;
+    unsigned* clear;
+    int clear_words;
+};
+cudaError_t launch_quantize(const QuantizeLaunch& a, cudaStream_t s, bool pdl = false);
+
+// A product of 8-bit activations and weights (int8_gemm.cu): the experts' gate_up (SwiGLU,
+// fp32 rows), the experts' down (scaled, weighted rows) or one dense product (bf16).
+struct Int8GemmLaunch {
+    enum Kind { kGateUp, kDown, kDense } kind;
+    const int8_t* w;         // gate_up [E, 2f, D], down [E, D, f], dense [D, f] (D = N, f = K)
+    const float* w_scale;    // one per weight row
+    const int8_t* act;       // gate_up: tokens [T, D]; down: h [rows, f]; dense: [rows, f]
+    const float* act_scale;  // one per row of act
+    const int32_t* offsets;  // [E+1], NULL: one dense group of `rows` rows
+    const int32_t* sorted_token;  // token of each row, NULL: identity
+    const float* sorted_w;        // down: weight of each row, NULL: 1
+    int rows, tokens, E, D, f;
+    float* h_out;    // gate_up
+    float* acc_out;  // down: [T, D] scatter-add target, or NULL
+    float* y_out;    // down: [rows, D], or NULL
+    bf16* y16_out;   // down: [rows, D], or NULL; dense: [rows, N]
+    int* status;
+    int8_t* gather_buf;  // gate_up: room for the rows in expert order [rows, D], or NULL
+    float* zero_acc;     // gate_up: cleared in the kernel (zero_floats a multiple of 4)
+    long long zero_floats;
+    int ksplit_max;      // as GroupedGemmLaunch; part holds int32 planes of [rows, 2f | N]
+    void* part;
+    unsigned* tickets;
+    int ticket_cap;
+};
+bool int8_gemm_uses_pairs(const Int8GemmLaunch& a, int num_sms);
+int int8_gemm_launches(const Int8GemmLaunch& a, int num_sms);
+cudaError_t launch_int8_gemm(const Int8GemmLaunch& a, int num_sms, cudaStream_t s, bool pdl);
 
 // expert parallelism (ep.cu): receive-side grouping and the return of the expert rows
 size_t ep_recv_layout_smem(int G, int El);

@@ -1,0 +1,157 @@
+// int8_gemm.cu -- products of 8-bit integers with a scale for each token and each weight row:
+//   y[t, n] = xs[t] ws[n] sum_k xq[t, k] wq[n, k]
+// grouped over experts (gate_up with SwiGLU, down with the routing weights) or dense, on the
+// kernels of grouped_gemm.cuh with tcgen05.mma.kind::i8: the sums are int32 and exact, the
+// scales are applied once per element in the epilogue.
+//
+// Against bf16 a weight takes half the bytes (what bounds few tokens: HBM) and the tensor
+// cores do twice the products (what bounds many tokens).  Tokens on M throughout: one-CTA
+// tiles of 128 tokens x 256 weight rows, K cut into slices when the tiles cannot fill the GPU,
+// and CTA pairs (256 x 256) once groups average 128 rows, as for bf16.
+#include <algorithm>
+
+#include "grouped_gemm.cuh"
+
+namespace moe {
+namespace {
+
+// Rows in expert order for the CTA-pair kernel: out[r] = x[tok[r]] for r < *row_count.
+__global__ void __launch_bounds__(256) gather_rows_i8_kernel(const uint4* x, const int32_t* tok,
+                                                             const int32_t* row_count, int rows,
+                                                             int vec, uint4* out) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const long long n = static_cast<long long>(row_count ? min(*row_count, rows) : rows) * vec;
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += 256ll * gridDim.x) {
+        const long long r = i / vec;
+        out[i] = __ldg(x + static_cast<long long>(__ldg(tok + r)) * vec + (i - r * vec));
+    }
+}
+
+bool use_pairs(const Int8GemmLaunch& a, int num_sms) {
+    const bool gathered = a.kind == Int8GemmLaunch::kGateUp && a.sorted_token != nullptr;
+    return num_sms >= 2 && a.rows / a.E >= 128 && (!gathered || a.gather_buf != nullptr);
+}
+
+template <bool GATE_UP>
+cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const Params& p, bool pair,
+                       int ctas, cudaStream_t s, bool pdl) {
+    const size_t ring = pair ? static_cast<size_t>(CfgPair::kStages) * CfgPair::kStageBytes
+                             : static_cast<size_t>(CfgTm::kStages) * CfgTm::kStageBytes;
+    const int stages = pair ? CfgPair::kStages : CfgTm::kStages;
+    const size_t smem = 1024 + ring + (2 * stages + 5) * 8 + 16 + 2 * (p.G + 1) * sizeof(int) +
+                        (GATE_UP ? 0 : kEpiStageBytes);
+    auto kfn = pair ? grouped_gemm_pair_kernel<GATE_UP, true> : grouped_gemm_tm_kernel<GATE_UP, true>;
+    cudaError_t err = set_smem_limit(reinterpret_cast<const void*>(kfn), smem);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kTmThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (pair) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = 2;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    if (pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    err = cudaLaunchKernelEx(&cfg, kfn, mw, ma, p);
+    count_launches(1);
+    return err;
+}
+
+}  // namespace
+
+bool int8_gemm_uses_pairs(const Int8GemmLaunch& a, int num_sms) { return use_pairs(a, num_sms); }
+
+int int8_gemm_launches(const Int8GemmLaunch& a, int num_sms) {
+    if (a.rows == 0) return 0;
+    return a.kind == Int8GemmLaunch::kGateUp && a.sorted_token && use_pairs(a, num_sms) ? 2 : 1;
+}
+
+cudaError_t launch_int8_gemm(const Int8GemmLaunch& a, int num_sms, cudaStream_t s, bool pdl) {
+    if (a.rows == 0) return cudaSuccess;
+    if (a.E > kMaxGroups) return cudaErrorInvalidValue;
+    const bool gate_up = a.kind == Int8GemmLaunch::kGateUp;
+    const bool dense = a.kind == Int8GemmLaunch::kDense;
+    const bool pair = use_pairs(a, num_sms);
+    const int K = gate_up ? a.D : a.f;  // 8-bit values; the tensor maps count pairs of them
+    const int w_group_rows = gate_up ? 2 * a.f : a.D;
+    bool gather = gate_up && a.sorted_token != nullptr;
+    const int8_t* act = a.act;
+    cudaError_t err;
+    if (pair && gather) {
+        const int vec = K / 16;
+        const long long n = static_cast<long long>(a.rows) * vec;
+        err = launch_kernel(gather_rows_i8_kernel,
+                            dim3(static_cast<unsigned>(std::min<long long>((n + 255) / 256, 8ll * num_sms))),
+                            dim3(256), 0, s, pdl, reinterpret_cast<const uint4*>(act), a.sorted_token,
+                            a.offsets ? a.offsets + a.E : nullptr, a.rows, vec,
+                            reinterpret_cast<uint4*>(a.gather_buf));
+        count_launches(1);
+        if (err != cudaSuccess) return err;
+        act = a.gather_buf;
+        gather = false;
+        pdl = true;
+    }
+    CUtensorMap mw, ma;
+    if ((err = encode_tile_map(&mw, a.w, static_cast<uint64_t>(w_group_rows) * a.E, K / 2, kBM)) !=
+        cudaSuccess)
+        return err;
+    // with a gather the activation map is not read: it covers the first row
+    if ((err = encode_tile_map(&ma, act, gather ? 1 : a.rows, K / 2, gather ? 1 : kTmRows)) != cudaSuccess)
+        return err;
+    Params p{};
+    p.offsets = a.offsets;
+    p.rows_total = a.rows;
+    p.sorted_token = a.sorted_token;
+    p.sorted_w = a.sorted_w;
+    p.G = a.E;
+    p.nf = gate_up ? a.f / kBM : ceil_div(a.D, kTmN);
+    p.nk = ceil_div(K, 2 * kBK);
+    p.w_group_rows = w_group_rows;
+    p.up_rows = a.f;
+    p.out_cols = gate_up ? a.f : a.D;
+    p.acc_out = a.acc_out;
+    p.y_out = a.y_out;
+    p.y16_out = a.y16_out;
+    p.status = a.status;
+    p.gather_tok = gather ? a.sorted_token : nullptr;
+    p.x = reinterpret_cast<const bf16*>(act);
+    p.ksplit = 1;
+    p.zero_acc = gate_up ? a.zero_acc : nullptr;
+    p.zero_n4 = a.zero_floats / 4;
+    p.row_scale = a.act_scale;
+    p.scale_tok = gate_up ? a.sorted_token : nullptr;
+    p.col_scale = a.w_scale;
+    p.h32_out = a.h_out;
+    p.dense = dense ? 1 : 0;
+    // gate_up and dense slices meet in the partial-sum planes; down's add into acc_out
+    const bool split = !pair && a.ksplit_max > 1 &&
+                       (a.kind == Int8GemmLaunch::kDown
+                            ? (a.acc_out != nullptr && a.y_out == nullptr && a.y16_out == nullptr)
+                            : (a.part != nullptr && a.tickets != nullptr && a.ticket_cap > 0));
+    p.ksplit_max = split ? std::min(a.ksplit_max, kSplitSlicesMax) : 1;
+    p.part = reinterpret_cast<float*>(a.part);
+    p.part_rows = a.rows;
+    p.tickets = a.tickets;
+    p.ticket_cap = a.ticket_cap;
+    // persistent: one CTA (or pair) per SM, fewer when the units cannot fill them
+    const int tile_rows = pair ? CfgPair::kPairRows : kTmRows;
+    const long long max_tiles = (static_cast<long long>(ceil_div(a.rows, tile_rows)) +
+                                 std::min(p.G, a.rows)) * p.nf * p.ksplit_max;
+    const int ctas = pair ? 2 * static_cast<int>(std::min<long long>(max_tiles, num_sms / 2))
+                          : static_cast<int>(std::min<long long>(max_tiles, num_sms));
+    return gate_up ? launch_one<true>(mw, ma, p, pair, ctas, s, pdl)
+                   : launch_one<false>(mw, ma, p, pair, ctas, s, pdl);
+}
+
+}  // namespace moe

@@ -8,7 +8,7 @@
 #include <mutex>
 #include <vector>
 
-#include "common.cuh"
+#include "api_util.cuh"
 
 namespace moe {
 
@@ -44,26 +44,6 @@ unsigned long long grid_wait_budget_ns() { return g_grid_wait_ns.load(std::memor
 
 namespace {
 
-constexpr size_t kAlign = 256;
-constexpr int kMaxDevices = 64;
-
-size_t align_up(size_t v) { return (v + kAlign - 1) & ~(kAlign - 1); }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int num_sms_current() {
-    static int cache[kMaxDevices] = {0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 148;
-    if (cache[dev] == 0) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-            n = 148;
-        cache[dev] = n;
-    }
-    return cache[dev];
-}
-
 // Workspace of the whole layer.  The status word is always at offset 0.
 struct Layout {
     size_t status, counters, counts, tickets, perm_hist, logits, offsets, dense_offsets, topk_idx,
@@ -71,20 +51,6 @@ struct Layout {
         part, total;
     size_t zero_end;  // [0, zero_end) is cleared at the start of a layer call
 };
-
-// The routed gate_up may cut its tiles' K steps into up to kSplitMax slices when its tiles
-// cannot fill the GPU (a few tokens, or a few experts), if the slices' fp32 partial sums
-// (kSplitMax planes of [T*K, 2f]) take at most 64 MiB; one ticket per tile, bounded by the
-// tiles of 16-row blocks: min(E, T*K) + T*K/16 + 1 row blocks of f/128 feature blocks.
-constexpr int kSplitMax = 4;
-bool gate_up_split_ok(long long T, long long K, long long f) {
-    return 4ll * kSplitMax * T * K * 2 * f <= (64ll << 20);
-}
-long long gate_up_ticket_cap(long long T, long long E, long long K, long long f) {
-    if (!gate_up_split_ok(T, K, f)) return 0;
-    const long long rows = T * K;
-    return (std::min(E, rows) + rows / 16 + 1) * (f / 128);
-}
 
 Layout layout(long long T, long long D, long long E, long long K, long long f, long long fs) {
     Layout L{};
@@ -125,22 +91,6 @@ Layout layout(long long T, long long D, long long E, long long K, long long f, l
     return L;
 }
 
-int check_shape(int T, int D, int E, int K, int f, int fs) {
-    if (T < 0 || D <= 0 || E <= 0 || K <= 0 || f <= 0 || fs < 0) return MOE_ERR_ARG;
-    if (E > 512 || K > 16 || K > E) return MOE_ERR_UNSUPPORTED;
-    if (D % 128 || D > 8192 || f % 128 || f > 8192 || fs % 128 || fs > 8192)
-        return MOE_ERR_UNSUPPORTED;
-    if (static_cast<long long>(T) * K >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
-    return MOE_OK;
-}
-
-inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
-
-template <class P>
-P* at(void* ws, size_t off) {
-    return reinterpret_cast<P*>(static_cast<uint8_t*>(ws) + off);
-}
-
 // Host checks of moe_layer_forward's parameters (out may be NULL when only planning).
 int check_layer(const moe_layer_params* p, const moe_bf16* out) {
     if (!p) return MOE_ERR_ARG;
@@ -173,7 +123,8 @@ struct LayerPlan {
     bool combine;    // a combine launch ends the call
 };
 
-LayerPlan plan_layer(const moe_layer_params* p, moe_bf16* out, void* workspace, int sms) {
+LayerPlan plan_layer(const moe_layer_params* p, moe_bf16* out, void* workspace, int sms,
+                     const RouteLogitsLaunch* rule = nullptr) {
     const int T = p->T, D = p->D, E = p->E, K = p->K, f = p->f, fs = p->f_s;
     const Layout L = layout(T, D, E, K, f, fs);
     const bool shared = fs > 0;
@@ -241,6 +192,7 @@ LayerPlan plan_layer(const moe_layer_params* p, moe_bf16* out, void* workspace, 
     r.score_mode = p->score_mode;
     r.select_bias = p->select_bias;
     r.bf16_weights = (p->flags & MOE_FLAG_BF16_WEIGHTS) ? 1 : 0;
+    r.rule = rule;
 
     GroupedGemmLaunch& up = q.up;
     up.gate_up = true;
@@ -518,6 +470,13 @@ int moe_combine(const float* out_acc, const float* y_sorted, const int32_t* slot
 
 int moe_layer_forward(const moe_layer_params* p, moe_bf16* out, void* workspace, size_t ws_bytes,
                       void* stream) {
+    return layer_forward(p, nullptr, out, workspace, ws_bytes, stream);
+}
+
+}  // extern "C"
+
+int moe::layer_forward(const moe_layer_params* p, const RouteLogitsLaunch* rule, moe_bf16* out,
+                       void* workspace, size_t ws_bytes, void* stream) {
     int rc = check_layer(p, out);
     if (rc) return rc;
     if (p->T > 0 && (!p->x || !out)) return MOE_ERR_ARG;
@@ -529,7 +488,7 @@ int moe_layer_forward(const moe_layer_params* p, moe_bf16* out, void* workspace,
 
     cudaStream_t s = as_stream(stream);
     const int sms = num_sms_current();
-    LayerPlan q = plan_layer(p, out, workspace, sms);
+    LayerPlan q = plan_layer(p, out, workspace, sms, rule);
     auto mark = [&](int i) {
         return p->step_events == nullptr || p->step_events[i] == nullptr ||
                cudaEventRecord(reinterpret_cast<cudaEvent_t>(p->step_events[i]), s) == cudaSuccess;
@@ -558,6 +517,8 @@ int moe_layer_forward(const moe_layer_params* p, moe_bf16* out, void* workspace,
     if (q.combine && launch_combine(q.c, sms, s, true) != cudaSuccess) return MOE_ERR_CUDA;
     return mark(MOE_EV_END) ? MOE_OK : MOE_ERR_CUDA;
 }
+
+extern "C" {
 
 int moe_layer_plan(const moe_layer_params* p, unsigned* step_mask, int* launches) {
     int rc = check_layer(p, nullptr);

@@ -324,6 +324,7 @@ router_kernel(RouterLaunch a, int experts_per_cta, int dsplit) {
             }
         }
     }
+    if (a.rule) return;  // only the logits are wanted
     __threadfence();  // this thread's logits are visible device-wide before the ticket
 
     // ---- ticket: the last CTA of this token block does the selection
@@ -349,6 +350,51 @@ router_kernel(RouterLaunch a, int experts_per_cta, int dsplit) {
 }
 
 
+// w_s . x_t by one warp (the sum in every lane)
+__device__ __forceinline__ float shared_gate_dot(const RouterLaunch& a, int token, int lane) {
+    const uint4* xv = reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(token) * a.D);
+    const uint4* wv = reinterpret_cast<const uint4*>(a.w_shared_gate);
+    float acc = 0.f;
+    // 8 chunks of x and w_s per lane in flight at a time (D = 4096 is 16 chunks a lane:
+    // two round trips to memory instead of sixteen)
+    constexpr int kBatch = 8;
+    for (int c0 = lane; c0 < a.D / 8; c0 += 32 * kBatch) {
+        uint4 x8[kBatch], w8[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int c = c0 + 32 * u;
+            const bool in = c < a.D / 8;
+            x8[u] = in ? __ldg(xv + c) : make_uint4(0, 0, 0, 0);
+            w8[u] = in ? __ldg(wv + c) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            acc = fmaf(bf16_lo(x8[u].x), bf16_lo(w8[u].x), acc);
+            acc = fmaf(bf16_hi(x8[u].x), bf16_hi(w8[u].x), acc);
+            acc = fmaf(bf16_lo(x8[u].y), bf16_lo(w8[u].y), acc);
+            acc = fmaf(bf16_hi(x8[u].y), bf16_hi(w8[u].y), acc);
+            acc = fmaf(bf16_lo(x8[u].z), bf16_lo(w8[u].z), acc);
+            acc = fmaf(bf16_hi(x8[u].z), bf16_hi(w8[u].z), acc);
+            acc = fmaf(bf16_lo(x8[u].w), bf16_lo(w8[u].w), acc);
+            acc = fmaf(bf16_hi(x8[u].w), bf16_hi(w8[u].w), acc);
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+    return acc;
+}
+
+// The shared gate alone, one warp per token (when the selection is launch_route_logits').
+__global__ void __launch_bounds__(kRouterThreads) shared_gate_kernel(RouterLaunch a) {
+    const int token = blockIdx.x * (kRouterThreads / 32) + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    grid_dep_wait();
+    grid_dep_launch();
+    if (token >= a.T) return;
+    const float acc = shared_gate_dot(a, token, lane);
+    if (lane == 0) a.shared_gate[token] = 1.f / (1.f + expf(-acc));
+}
+
 // Selection after the tensor-core logits: one warp per token over the partial logit
 // planes (no bias yet), the planes added in order and the bias on load; the shared gate's
 // dot product w_s . x_t is done here by the same warp.  (The layer's accumulator is
@@ -364,43 +410,40 @@ __global__ void __launch_bounds__(kRouterThreads, 4) router_select_kernel(Router
     select_topk_warp(a.logits + static_cast<size_t>(token) * a.E, a.logit_planes,
                      static_cast<size_t>(a.T) * a.E, a.logit_bias, a, token, lane);
     if (a.w_shared_gate) {
-        const uint4* xv = reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(token) * a.D);
-        const uint4* wv = reinterpret_cast<const uint4*>(a.w_shared_gate);
-        float acc = 0.f;
-        // 8 chunks of x and w_s per lane in flight at a time (D = 4096 is 16 chunks a lane:
-        // two round trips to memory instead of sixteen)
-        constexpr int kBatch = 8;
-        for (int c0 = lane; c0 < a.D / 8; c0 += 32 * kBatch) {
-            uint4 x8[kBatch], w8[kBatch];
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int c = c0 + 32 * u;
-                const bool in = c < a.D / 8;
-                x8[u] = in ? __ldg(xv + c) : make_uint4(0, 0, 0, 0);
-                w8[u] = in ? __ldg(wv + c) : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                acc = fmaf(bf16_lo(x8[u].x), bf16_lo(w8[u].x), acc);
-                acc = fmaf(bf16_hi(x8[u].x), bf16_hi(w8[u].x), acc);
-                acc = fmaf(bf16_lo(x8[u].y), bf16_lo(w8[u].y), acc);
-                acc = fmaf(bf16_hi(x8[u].y), bf16_hi(w8[u].y), acc);
-                acc = fmaf(bf16_lo(x8[u].z), bf16_lo(w8[u].z), acc);
-                acc = fmaf(bf16_hi(x8[u].z), bf16_hi(w8[u].z), acc);
-                acc = fmaf(bf16_lo(x8[u].w), bf16_lo(w8[u].w), acc);
-                acc = fmaf(bf16_hi(x8[u].w), bf16_hi(w8[u].w), acc);
-            }
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+        const float acc = shared_gate_dot(a, token, lane);
         if (lane == 0) a.shared_gate[token] = 1.f / (1.f + expf(-acc));
     }
 }
 
+// After the logits: the caller's rule (planes of partial sums row_stride and plane_stride
+// floats apart) and, with a shared expert, its gate.
+cudaError_t launch_rule(const RouterLaunch& a, long long row_stride, int planes,
+                        const float* logit_bias, int num_sms, cudaStream_t s) {
+    RouteLogitsLaunch r = *a.rule;
+    r.logits = a.logits;
+    r.is_bf16 = false;
+    r.row_stride = row_stride;
+    r.planes = planes;
+    r.plane_stride = static_cast<long long>(a.T) * row_stride;
+    r.logit_bias = logit_bias;
+    r.T = a.T; r.E = a.E; r.K = a.K;
+    r.topk_idx = a.topk_idx;
+    r.topk_w = a.topk_w;
+    r.counts = a.counts;
+    cudaError_t err = launch_route_logits(r, num_sms, s);
+    if (err != cudaSuccess || a.w_shared_gate == nullptr) return err;
+    err = launch_kernel(shared_gate_kernel, dim3(ceil_div(a.T, kRouterThreads / 32)),
+                        dim3(kRouterThreads), 0, s, true, a);
+    count_launches(1);
+    return err;
+}
+
 }  // namespace
 
-cudaError_t launch_router(const RouterLaunch& a, int num_sms, cudaStream_t s, bool pdl) {
-    if (a.T == 0) return cudaSuccess;
+cudaError_t launch_router(const RouterLaunch& in, int num_sms, cudaStream_t s, bool pdl) {
+    if (in.T == 0) return cudaSuccess;
+    RouterLaunch a = in;
+    if (a.rule) a.w_shared_gate = nullptr;
     const int n_tb = ceil_div(a.T, kTokensPerCta);
     const int rows_total = a.E + (a.w_shared_gate ? 1 : 0);
     // Few token blocks: the dot products of an expert pair are split over dsplit warps (a
@@ -423,7 +466,8 @@ cudaError_t launch_router(const RouterLaunch& a, int num_sms, cudaStream_t s, bo
     err = launch_kernel(router_kernel, dim3(n_tb, n_eb), dim3(kRouterThreads), smem, s, pdl, a,
                         per_cta, dsplit);
     count_launches(1);
-    return err;
+    if (err != cudaSuccess || !a.rule) return err;
+    return launch_rule(in, a.E + 1, 1, nullptr, num_sms, s);
 }
 
 
@@ -467,6 +511,7 @@ cudaError_t launch_router_tc(const RouterLaunch& a, int num_sms, cudaStream_t s,
     g.ksplit = S;
     cudaError_t err = launch_grouped_gemm(g, num_sms, s, pdl);
     if (err != cudaSuccess) return err;
+    if (a.rule) return launch_rule(a, a.E, S, a.logit_bias, num_sms, s);
     RouterLaunch sel = a;
     sel.logit_planes = S;
     err = launch_kernel(router_select_kernel, dim3(ceil_div(a.T, kRouterThreads / 32)),
