@@ -308,41 +308,48 @@ def _need(ok: bool, what: str):
         raise MoEError(-1, what)
 
 
+_get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _on_device_of(fn):
     """Runs fn with its first argument's device current and its ``stream`` (default: that
     device's current stream) as the current one, so that what fn allocates belongs to it."""
     @functools.wraps(fn)
     def call(first, *args, stream=None, **kw):
-        if not first.is_cuda:
+        index = first.get_device()
+        if index < 0:
             raise ValueError("expected a CUDA tensor")
-        dev = first.device
-        if stream is None and dev.index == torch.cuda.current_device():
+        if stream is None and index == _get_device():
             return fn(first, *args, **kw)
         if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        if stream.device != dev:
-            raise ValueError(f"stream on {stream.device}, tensors on {dev}")
+            stream = torch.cuda.current_stream(index)
+        if stream.device != first.device:
+            raise ValueError(f"stream on {stream.device}, tensors on {first.device}")
         with torch.cuda.stream(stream):
             return fn(first, *args, **kw)
     return call
 
 
-def _q(t, dtype, dev):
-    """_p for a tensor that has to live on ``dev``."""
-    if t is not None and t.device != dev:
-        raise ValueError(f"expected a tensor on {dev}, got one on {t.device}")
-    return _p(t, dtype)
+def _q(t, dtype, index):
+    """Address of a contiguous tensor of type ``dtype`` on CUDA device ``index`` (None -> NULL)."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    if t.is_cuda and t.get_device() != index:
+        raise ValueError(f"expected a tensor on cuda:{index}, got one on {t.device}")
+    return _p(t, dtype)  # says what is wrong
 
 
 def route_rule(E, K, score="softmax", select_bias=None, n_group=1, topk_group=1, group_top=None,
-               renorm=True, scale=1.0, device=None) -> RouteRule:
+               renorm=True, scale=1.0) -> RouteRule:
     """A moe_route_rule.  group_top defaults to 2 with a select_bias (a group is judged by its two
     best keys) and 1 without."""
     if select_bias is not None:
         _need(select_bias.shape == (E,), "route_rule (select_bias must be [E])")
     if group_top is None:
         group_top = 1 if select_bias is None else 2
-    bias = _p(select_bias, F32) if device is None else _q(select_bias, F32, device)
+    bias = None if select_bias is None else _q(select_bias, F32, select_bias.get_device())
     rule = RouteRule(SCORES[score], bias, n_group, topk_group, group_top, 1 if renorm else 0, scale)
     rule.keep = select_bias  # the rule holds a bare pointer to it
     return rule
@@ -357,16 +364,17 @@ def route_logits(logits, K, score="softmax", select_bias=None, n_group=1, topk_g
     expert_counts [E] int32)."""
     _need(logits.dim() == 2, "route_logits (logits must be [T, E])")
     T, E = logits.shape
-    dev = logits.device
-    if logits.dtype is not F32 and logits.dtype is not BF16:
-        raise TypeError(f"expected fp32 or bf16 logits, got {logits.dtype}")
-    rule = route_rule(E, K, score, select_bias, n_group, topk_group, group_top, renorm, scale, dev)
-    idx = torch.empty((T, K), dtype=I32, device=dev)
-    w = torch.empty((T, K), dtype=F32, device=dev)
-    counts = torch.empty((E,), dtype=I32, device=dev)
-    _check(lib().moe_route_logits(_p(logits), 0 if logits.dtype is F32 else 1, T, E, K, rule,
-                                  idx.data_ptr(), w.data_ptr(), counts.data_ptr(), _stream()),
-           "moe_route_logits")
+    dev = logits.get_device()
+    kind = 0 if logits.dtype is F32 else 1
+    rule = route_rule(E, K, score, select_bias, n_group, topk_group, group_top, renorm, scale)
+    if select_bias is not None:
+        _q(select_bias, F32, dev)
+    x = _q(logits, F32 if kind == 0 else BF16, dev)
+    idx = logits.new_empty((T, K), dtype=I32)
+    w = logits.new_empty((T, K), dtype=F32)
+    counts = logits.new_empty((E,), dtype=I32)
+    _check(lib().moe_route_logits(x, kind, T, E, K, rule, idx.data_ptr(), w.data_ptr(),
+                                  counts.data_ptr(), _raw_stream(dev)), "moe_route_logits")
     return idx, w, counts
 
 
@@ -375,21 +383,24 @@ def quantize_rows(x):
     """Rows of x [..., C] bf16 as 8-bit integers: (q int8 like x, scale [...] f32) with
     x ~ q * scale (moe_quantize_rows)."""
     _need(x.dim() >= 1, "quantize_rows (x must have rows)")
-    C = x.shape[-1]
-    q = torch.empty(x.shape, dtype=I8, device=x.device)
-    scale = torch.empty(x.shape[:-1], dtype=F32, device=x.device)
-    _check(lib().moe_quantize_rows(_p(x, BF16), scale.numel(), C, q.data_ptr(), scale.data_ptr(),
-                                   _stream()), "moe_quantize_rows")
+    dev = x.get_device()
+    p = _q(x, BF16, dev)
+    q = x.new_empty(x.shape, dtype=I8)
+    scale = x.new_empty(x.shape[:-1], dtype=F32)
+    _check(lib().moe_quantize_rows(p, scale.numel(), x.shape[-1], q.data_ptr(), scale.data_ptr(),
+                                   _raw_stream(dev)), "moe_quantize_rows")
     return q, scale
 
 
-def _int8_workspace(T, N, K, dev, workspace):
+def _int8_buffers(x, T, N, K, out, workspace):
     n = int(lib().moe_int8_workspace_size(T, N, K))
     if n == 0:
         raise MoEError(-2, "moe_int8_workspace_size")
-    if workspace is None:
-        return torch.empty(n, dtype=U8, device=dev)
-    return workspace
+    if out is None:
+        out = x.new_empty((T, N), dtype=BF16)
+    else:
+        _need(out.shape == (T, N), "int8 product (out must be [T, N])")
+    return out, x.new_empty((n,), dtype=U8) if workspace is None else workspace
 
 
 @_on_device_of
@@ -398,14 +409,12 @@ def int8_matmul(xq, x_scale, wq, w_scale, workspace=None, out=None):
     wq [N, K] int8 (moe_int8_matmul)."""
     _need(xq.dim() == 2 and wq.dim() == 2 and xq.shape[1] == wq.shape[1],
           "int8_matmul (xq must be [T, K], wq [N, K])")
-    (T, K), N, dev = xq.shape, wq.shape[0], xq.device
+    (T, K), N, dev = xq.shape, wq.shape[0], xq.get_device()
     _need(x_scale.shape == (T,) and w_scale.shape == (N,), "int8_matmul (one scale per row)")
-    out = torch.empty((T, N), dtype=BF16, device=dev) if out is None else out
-    _need(out.shape == (T, N), "int8_matmul (out must be [T, N])")
-    ws = _int8_workspace(T, N, K, dev, workspace)
-    _check(lib().moe_int8_matmul(_p(xq, I8), _q(x_scale, F32, dev), _q(wq, I8, dev),
-                                 _q(w_scale, F32, dev), T, N, K, _q(out, BF16, dev),
-                                 _q(ws, U8, dev), ws.numel(), _stream()), "moe_int8_matmul")
+    a = _q(xq, I8, dev), _q(x_scale, F32, dev), _q(wq, I8, dev), _q(w_scale, F32, dev)
+    out, ws = _int8_buffers(xq, T, N, K, out, workspace)
+    _check(lib().moe_int8_matmul(*a, T, N, K, _q(out, BF16, dev), _q(ws, U8, dev), ws.numel(),
+                                 _raw_stream(dev)), "moe_int8_matmul")
     return out
 
 
@@ -415,14 +424,12 @@ def int8_linear(x, wq, w_scale, workspace=None, out=None):
     with w_scale [N]; returns [T, N] bf16 (moe_int8_linear)."""
     _need(x.dim() == 2 and wq.dim() == 2 and x.shape[1] == wq.shape[1],
           "int8_linear (x must be [T, K], wq [N, K])")
-    (T, K), N, dev = x.shape, wq.shape[0], x.device
+    (T, K), N, dev = x.shape, wq.shape[0], x.get_device()
     _need(w_scale.shape == (N,), "int8_linear (one scale per weight row)")
-    out = torch.empty((T, N), dtype=BF16, device=dev) if out is None else out
-    _need(out.shape == (T, N), "int8_linear (out must be [T, N])")
-    ws = _int8_workspace(T, N, K, dev, workspace)
-    _check(lib().moe_int8_linear(_p(x, BF16), _q(wq, I8, dev), _q(w_scale, F32, dev), T, N, K,
-                                 _q(out, BF16, dev), _q(ws, U8, dev), ws.numel(), _stream()),
-           "moe_int8_linear")
+    a = _q(x, BF16, dev), _q(wq, I8, dev), _q(w_scale, F32, dev)
+    out, ws = _int8_buffers(x, T, N, K, out, workspace)
+    _check(lib().moe_int8_linear(*a, T, N, K, _q(out, BF16, dev), _q(ws, U8, dev), ws.numel(),
+                                 _raw_stream(dev)), "moe_int8_linear")
     return out
 
 
@@ -434,34 +441,37 @@ def experts_int8(xq, x_scale, topk_w, perm, w_gate_up, gate_up_scale, w_down, do
     gate_up_scale [E, 2f] and down_scale [E, D], for the routing weights topk_w [T, K] and
     ``perm`` = permute(...).  Returns out [T, D] bf16 (+ residual).  Rows of ``perm`` are trusted:
     they must index the T tokens and the E experts."""
-    _need(xq.dim() == 2 and w_gate_up.dim() == 3 and w_down.dim() == 3 and topk_w.dim() == 2,
+    _need(xq.dim() == 2 and w_down.dim() == 3 and topk_w.dim() == 2,
           "experts_int8 (xq [T, D], topk_w [T, K], w_gate_up [E, 2f, D], w_down [E, D, f])")
     T, D = xq.shape
     E, _, f = w_down.shape
-    K, dev = topk_w.shape[1], xq.device
+    K, dev = topk_w.shape[1], xq.get_device()
     _need(topk_w.shape[0] == T and w_down.shape[1] == D and w_gate_up.shape == (E, 2 * f, D),
           "experts_int8 (weights and tokens of different shapes)")
     _need(x_scale.shape == (T,) and gate_up_scale.shape == (E, 2 * f)
           and down_scale.shape == (E, D), "experts_int8 (one scale per row)")
-    _need(perm["offsets"].numel() == E + 1 and perm["sorted_token"].numel() == T * K
-          and perm["sorted_w"].numel() == T * K and perm["slot_to_row"].numel() == T * K,
-          "experts_int8 (perm of another routing)")
-    out = torch.empty((T, D), dtype=BF16, device=dev) if out is None else out
-    _need(out.shape == (T, D) and (residual is None or residual.shape == (T, D)),
+    offsets, token, weight, row = (perm["offsets"], perm["sorted_token"], perm["sorted_w"],
+                                   perm["slot_to_row"])
+    n = T * K
+    _need(offsets.numel() == E + 1 and token.numel() == n and weight.numel() == n
+          and row.numel() == n, "experts_int8 (perm of another routing)")
+    _need((out is None or out.shape == (T, D)) and (residual is None or residual.shape == (T, D)),
           "experts_int8 (out and residual must be [T, D])")
     flags = MOE_FLAG_DETERMINISTIC if deterministic else 0
+    prm = Int8Experts(_q(xq, I8, dev), _q(x_scale, F32, dev), _q(offsets, I32, dev),
+                      _q(token, I32, dev), _q(weight, F32, dev), _q(row, I32, dev),
+                      _q(topk_w, F32, dev), _q(w_gate_up, I8, dev), _q(gate_up_scale, F32, dev),
+                      _q(w_down, I8, dev), _q(down_scale, F32, dev), _q(residual, BF16, dev),
+                      T, D, E, K, f, flags)
     if workspace is None:
         n = int(lib().moe_experts_int8_workspace_size(T, D, E, K, f, flags))
         if n == 0:
             raise MoEError(-2, "moe_experts_int8_workspace_size")
-        workspace = torch.empty(n, dtype=U8, device=dev)
-    prm = Int8Experts(_p(xq, I8), _q(x_scale, F32, dev), _q(perm["offsets"], I32, dev),
-                      _q(perm["sorted_token"], I32, dev), _q(perm["sorted_w"], F32, dev),
-                      _q(perm["slot_to_row"], I32, dev), _q(topk_w, F32, dev),
-                      _q(w_gate_up, I8, dev), _q(gate_up_scale, F32, dev), _q(w_down, I8, dev),
-                      _q(down_scale, F32, dev), _q(residual, BF16, dev), T, D, E, K, f, flags)
+        workspace = xq.new_empty((n,), dtype=U8)
+    if out is None:
+        out = xq.new_empty((T, D), dtype=BF16)
     _check(lib().moe_experts_int8(prm, _q(out, BF16, dev), _q(workspace, U8, dev),
-                                  workspace.numel(), _stream()), "moe_experts_int8")
+                                  workspace.numel(), _raw_stream(dev)), "moe_experts_int8")
     return out
 
 

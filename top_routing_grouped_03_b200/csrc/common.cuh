@@ -152,7 +152,7 @@ struct RouteLogitsLaunch {
     float* topk_w;
     int32_t* counts;          // [E] overwritten, or NULL
     // filled in by the launcher
-    int group_lanes, group_magic;
+    int group_lanes, group_magic, whole_registers;
 };
 cudaError_t launch_route_logits(const RouteLogitsLaunch& a, int num_sms, cudaStream_t s,
                                 bool pdl = false);
@@ -224,7 +224,7 @@ cudaError_t encode_tile_map(CUtensorMap* m, const void* base, uint64_t rows, uin
 
 // q[r, c] = rint(127 x[r, c] / amax_r), scale[r] = amax_r / 127 (quantize.cu).  A row with a NaN or an
 // infinity gets scale NaN and q = 0.  row_count (device, or NULL): rows past *row_count are
-// left alone.  clear (or NULL): clear_words 4-byte words set to 0 on the way.
+// left alone.  clear (or NULL): clear_words 4-byte words set to 0.
 struct QuantizeLaunch {
     const void* x;       // [rows, cols] bf16, or fp32 when is_f32
     bool is_f32;
@@ -250,7 +250,7 @@ struct Int8GemmLaunch {
     const int32_t* sorted_token;  // token of each row, NULL: identity
     const float* sorted_w;        // down: weight of each row, NULL: 1
     int rows, tokens, E, D, f;
-    float* h_out;    // gate_up
+    float* h_out;    // gate_up: fp32 rows of h
     float* acc_out;  // down: [T, D] scatter-add target, or NULL
     float* y_out;    // down: [rows, D], or NULL
     bf16* y16_out;   // down: [rows, D], or NULL; dense: [rows, N]
@@ -263,8 +263,6 @@ struct Int8GemmLaunch {
     unsigned* tickets;
     int ticket_cap;
 };
-bool int8_gemm_uses_pairs(const Int8GemmLaunch& a, int num_sms);
-int int8_gemm_launches(const Int8GemmLaunch& a, int num_sms);
 cudaError_t launch_int8_gemm(const Int8GemmLaunch& a, int num_sms, cudaStream_t s, bool pdl);
 
 // expert parallelism (ep.cu): receive-side grouping and the return of the expert rows

@@ -779,11 +779,12 @@ __device__ __forceinline__ void split_fixup_tile(const Params& p, int row0, int 
 // the weight row's fp32 scales.
 
 // v[j] (int32 bits) -> fp32 bits of v[j] * cs[j]; cs: 16-byte aligned, the same for all lanes
+// (the warp's copy of its columns' scales in shared memory, see stage_scales, or global)
 template <int N>
 __device__ __forceinline__ void scale_columns(uint32_t* v, const float* cs) {
 #pragma unroll
     for (int j = 0; j < N; j += 4) {
-        const float4 c = __ldg(reinterpret_cast<const float4*>(cs + j));
+        const float4 c = *reinterpret_cast<const float4*>(cs + j);
         v[j] = __float_as_uint(__int2float_rn(static_cast<int>(v[j])) * c.x);
         v[j + 1] = __float_as_uint(__int2float_rn(static_cast<int>(v[j + 1])) * c.y);
         v[j + 2] = __float_as_uint(__int2float_rn(static_cast<int>(v[j + 2])) * c.z);
@@ -800,29 +801,48 @@ __device__ __forceinline__ float row_scale_of(const Params& p, int row) {
     return __ldg(p.row_scale + (p.scale_tok ? __ldg(p.scale_tok + row) : row));
 }
 
-// gate_up: h (fp32) of the warp's 32 rows x hc features; wr: the tile's first gate row among
-// all weight rows, feat: its feature inside the group (both of this warp's first column).
+// The column scales of a warp's share of a tile into its 128 floats of shared memory: gate_up
+// 64 gate and 64 up features, otherwise 128 output columns.  Issued before the wait for the
+// accumulator, so that the loads (weights' scales come from HBM) overlap the products.
+constexpr int kScaleFloats = 128;
+template <bool GATE_UP>
+__device__ __forceinline__ void stage_scales(const Params& p, float* dst, int wr, int col0, int half,
+                                             int lane) {
+    const float* src;
+    bool in = true;
+    if (GATE_UP) {
+        src = p.col_scale + wr + half * 64 + (lane < 16 ? 4 * lane : p.up_rows + 4 * (lane - 16));
+    } else {
+        src = p.col_scale + wr + half * 128 + 4 * lane;
+        in = col0 + half * 128 + 4 * lane < p.out_cols;
+    }
+    __syncwarp();  // the last tile's reads are over
+    if (in) *reinterpret_cast<float4*>(dst + 4 * lane) = __ldg(reinterpret_cast<const float4*>(src));
+    __syncwarp();
+}
+
+// gate_up: h (fp32) of the warp's 32 rows x 64 features from feature feat on; rs: the row's scale.
 __device__ __forceinline__ void i8_gate_up_epilogue(const Params& p, uint32_t tgate, uint32_t tup,
-                                                    int row, bool valid, int wr, int feat, int hc) {
-    const float rs = valid ? row_scale_of(p, row) : 0.f;
+                                                    int row, bool valid, float rs, int feat,
+                                                    const float* scales) {
     float* hrow = p.h32_out + static_cast<size_t>(row) * p.out_cols + feat;
 #pragma unroll 1
-    for (int c0 = 0; c0 < hc; c0 += 16) {
+    for (int c0 = 0; c0 < 64; c0 += 16) {
         uint32_t gv[16], uv[16];
         tmem_ld16(tgate + c0, gv);
         tmem_ld16(tup + c0, uv);
         tmem_ld_wait();
-        scale_columns<16>(gv, p.col_scale + wr + c0);
-        scale_columns<16>(uv, p.col_scale + wr + p.up_rows + c0);
+        scale_columns<16>(gv, scales + c0);
+        scale_columns<16>(uv, scales + 64 + c0);
         if (valid) {
             float4* dst = reinterpret_cast<float4*>(hrow + c0);
 #pragma unroll
             for (int j = 0; j < 16; j += 4)
-                dst[j / 4] = make_float4(
+                __stcg(dst + j / 4, make_float4(
                     swiglu_scaled(__uint_as_float(gv[j]), __uint_as_float(uv[j]), rs),
                     swiglu_scaled(__uint_as_float(gv[j + 1]), __uint_as_float(uv[j + 1]), rs),
                     swiglu_scaled(__uint_as_float(gv[j + 2]), __uint_as_float(uv[j + 2]), rs),
-                    swiglu_scaled(__uint_as_float(gv[j + 3]), __uint_as_float(uv[j + 3]), rs));
+                    swiglu_scaled(__uint_as_float(gv[j + 3]), __uint_as_float(uv[j + 3]), rs)));
         }
     }
 }
@@ -846,8 +866,7 @@ __device__ __forceinline__ void i8_store_partials(uint32_t tcol, float* prow, in
 
 // Dense product: bf16 rows of cols columns (a multiple of 8).
 __device__ __forceinline__ void i8_dense_epilogue(const Params& p, uint32_t tcol, int row, bool valid,
-                                                  int col0, int cols) {
-    const float rs = valid ? row_scale_of(p, row) : 0.f;
+                                                  float rs, int col0, int cols, const float* scales) {
     bf16* orow = p.y16_out + static_cast<size_t>(row) * p.out_cols + col0;
 #pragma unroll 1
     for (int c0 = 0; c0 < cols; c0 += 16) {
@@ -857,7 +876,7 @@ __device__ __forceinline__ void i8_dense_epilogue(const Params& p, uint32_t tcol
 #pragma unroll
         for (int h = 0; h < 16; h += 8) {
             if (c0 + h >= cols) break;
-            scale_columns<8>(v + h, p.col_scale + col0 + c0 + h);
+            scale_columns<8>(v + h, scales + c0 + h);
             if (valid)
                 *reinterpret_cast<uint4*>(orow + c0 + h) = make_uint4(
                     pack_bf16x2(rs * __uint_as_float(v[h]), rs * __uint_as_float(v[h + 1])),
@@ -923,12 +942,16 @@ __device__ __forceinline__ void i8_split_fixup(const Params& p, int row0, int ro
 // tile's wn/2; down: output columns [wn/2 half, wn/2 (half + 1)) of its wn).  The warp's
 // 32 lanes are 32 rows.
 // ROWS16: the kernel may write bf16 rows (p.y16_out; the CTA-pair kernel only).
-// I8: int32 accumulators; wr is the tile's first weight row among all groups.
+// I8: int32 accumulators; rs is the row's scale (down: times its weight), scales the warp's
+// column scales.
 template <bool GATE_UP, bool ROWS16 = false, bool I8 = false>
 __device__ __forceinline__ void tm_epilogue(const Params& p, uint32_t tbase, int row, bool valid,
                                             int tile_i, int half, float* stage, int wn,
-                                            float* part = nullptr, int wr = 0) {
+                                            float* part = nullptr, float rs = 1.f,
+                                            const float* scales = nullptr) {
     const int lane = threadIdx.x & 31;
+    // few rows in the tile: a warp without any has nothing to drain
+    if (I8 && __ballot_sync(0xffffffffu, valid) == 0) return;
     if (I8 && GATE_UP) {
         const int F = wn >> 1, hc = F >> 1, feat = tile_i * F + half * hc;
         if (part) {
@@ -936,8 +959,8 @@ __device__ __forceinline__ void tm_epilogue(const Params& p, uint32_t tbase, int
             i8_store_partials(tbase + half * hc, prow, hc, valid);
             i8_store_partials(tbase + F + half * hc, prow + p.out_cols, hc, valid);
         } else {
-            i8_gate_up_epilogue(p, tbase + half * hc, tbase + F + half * hc, row, valid,
-                                wr + half * hc, feat, hc);
+            i8_gate_up_epilogue(p, tbase + half * hc, tbase + F + half * hc, row, valid, rs, feat,
+                                scales);
         }
     } else if (I8 && p.dense) {
         // dense product; the last tile may hold fewer than wn columns
@@ -948,7 +971,7 @@ __device__ __forceinline__ void tm_epilogue(const Params& p, uint32_t tbase, int
             i8_store_partials(tbase + half * hc, part + static_cast<size_t>(row) * p.out_cols + col0,
                               cols, valid);
         else
-            i8_dense_epilogue(p, tbase + half * hc, row, valid, col0, cols);
+            i8_dense_epilogue(p, tbase + half * hc, row, valid, rs, col0, cols, scales);
     } else if (GATE_UP && part) {
         // one K slice of the tile: fp32 partial sums of the gate and up features
         const int F = wn >> 1;
@@ -1000,9 +1023,8 @@ __device__ __forceinline__ void tm_epilogue(const Params& p, uint32_t tbase, int
         // the last tile of an int8 launch may hold half the columns (out_cols is a multiple
         // of 128, the tile of 256)
         if (I8 && tile_i * wn + half * hc >= p.out_cols) return;
-        float w = (valid && p.sorted_w) ? __ldg(p.sorted_w + row) : 1.f;
-        if (I8 && valid) w *= __ldg(p.row_scale + row);
-        const float* cs = I8 ? p.col_scale + wr + half * hc : nullptr;
+        const float w = I8 ? rs : (valid && p.sorted_w) ? __ldg(p.sorted_w + row) : 1.f;
+        const float* cs = scales;
         const int tok = valid ? (p.sorted_token ? __ldg(p.sorted_token + row) : row) : 0;
         const int col0 = tile_i * wn + half * hc;
         const uint32_t tcol = tbase + half * hc;
@@ -1086,6 +1108,24 @@ constexpr size_t kEpiStageBytes = 16 + (kTmEpiThreads / 32) * kStageFloatsPerWar
 __device__ __forceinline__ float* epi_stage(int* table_end, int warp) {
     const uintptr_t a = (reinterpret_cast<uintptr_t>(table_end) + 15) & ~static_cast<uintptr_t>(15);
     return reinterpret_cast<float*>(a) + (warp - 2) * kStageFloatsPerWarp;
+}
+
+// int8 kernels: the warps' column scales, after that staging (down) or the group table (gate_up)
+constexpr size_t kScaleBytes = (kTmEpiThreads / 32) * kScaleFloats * sizeof(float);
+template <bool GATE_UP>
+__device__ __forceinline__ float* scale_stage(int* table_end, int warp) {
+    float* base = epi_stage(table_end, 2);
+    if (!GATE_UP) base += (kTmEpiThreads / 32) * kStageFloatsPerWarp;
+    return base + (warp - 2) * kScaleFloats;
+}
+
+// The scale that a row's products get: gate_up and dense the token's, down the row's own times
+// its routing weight.
+template <bool GATE_UP>
+__device__ __forceinline__ float i8_row_scale(const Params& p, int row) {
+    float s = row_scale_of(p, row);
+    if (!GATE_UP && p.sorted_w) s *= __ldg(p.sorted_w + row);
+    return s;
 }
 
 struct CfgTm {
@@ -1266,10 +1306,20 @@ grouped_gemm_tm_kernel(const __grid_constant__ CUtensorMap map_w,
         // ---------------------------------------------------------------- epilogue
         const int q = warp & 3;
         if (GATE_UP) clear_accumulator(p, threadIdx.x - 64, kTmEpiThreads);
+        float* scales = I8 ? scale_stage<GATE_UP>(g_tile + p.G + 1, warp) : nullptr;
         uint32_t abuf = 0, aphase = 0;
         for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
             const Unit un = unit_at(units, tile);
             const Tile t = decode_tile(un.tile, g_tile, g_off, p.G, kTmRows);
+            const int row = t.row0 + q * 32 + lane;
+            const bool valid = row < t.row_end;
+            const int half = (warp - 2) >> 2;
+            const int wr = t.g * p.w_group_rows + t.i * (GATE_UP ? kBM : kTmN);
+            float rs = 1.f;
+            if (I8) {
+                rs = valid ? i8_row_scale<GATE_UP>(p, row) : 0.f;
+                stage_scales<GATE_UP>(p, scales, wr, t.i * kTmN, half, lane);
+            }
             const bool ready = mbar_wait(&tfull[abuf], aphase, kWaitBudgetNs, abort_flag);
             if (!epilogue_bar_and<kTmEpiThreads>(ready)) {
                 set_status(p.status, MOE_ERR_TIMEOUT);
@@ -1279,9 +1329,6 @@ grouped_gemm_tm_kernel(const __grid_constant__ CUtensorMap map_w,
             tc_fence_after();
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    abuf * C::kAccCols;
-            const int row = t.row0 + q * 32 + lane;
-            const bool valid = row < t.row_end;
-            const int half = (warp - 2) >> 2;
             // gate_up cut into slices: this slice's partial sums, [row][gate f | up f]
             // (dense int8 product: [row][N])
             const bool meets = GATE_UP || (I8 && p.dense);
@@ -1289,10 +1336,9 @@ grouped_gemm_tm_kernel(const __grid_constant__ CUtensorMap map_w,
                               ? p.part + static_cast<size_t>(un.slice) * p.part_rows *
                                              (GATE_UP ? 2 : 1) * p.out_cols
                               : nullptr;
-            const int wr = t.g * p.w_group_rows + t.i * (GATE_UP ? kBM : kTmN);
             tm_epilogue<GATE_UP, false, I8>(
                 p, tbase, row, valid, t.i, half,
-                GATE_UP ? nullptr : epi_stage(g_tile + p.G + 1, warp), kTmN, part, wr);
+                GATE_UP ? nullptr : epi_stage(g_tile + p.G + 1, warp), kTmN, part, rs, scales);
             tc_fence_before();
             mbar_arrive(&tempty[abuf]);
             abuf ^= 1u;
@@ -1497,9 +1543,18 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w,
         const int q = warp & 3;
         if (GATE_UP) clear_accumulator(p, threadIdx.x - 64, kTmEpiThreads);
         const uint32_t leader_tempty0 = map_to_rank(smem_u32(&tempty[0]), 0);
+        float* scales = I8 ? scale_stage<GATE_UP>(g_tile + p.G + 1, warp) : nullptr;
         uint32_t abuf = 0, aphase = 0;
         for (int tile = pair; tile < total; tile += npairs) {
             const Tile t = decode_tile(tile, g_tile, g_off, p.G, C::kPairRows);
+            const int row = t.row0 + static_cast<int>(rank) * kTmRows + q * 32 + lane;
+            const int half = (warp - 2) >> 2;
+            float rs = 1.f;
+            if (I8) {
+                rs = row < t.row_end ? i8_row_scale<GATE_UP>(p, row) : 0.f;
+                stage_scales<GATE_UP>(p, scales, t.g * p.w_group_rows + t.i * (GATE_UP ? kBM : kTmN),
+                                      t.i * kTmN, half, lane);
+            }
             const bool ready = mbar_wait(&tfull[abuf], aphase, kWaitBudgetNs, abort_flag);
             if (!epilogue_bar_and<kTmEpiThreads>(ready)) {
                 set_status(p.status, MOE_ERR_TIMEOUT);
@@ -1509,11 +1564,9 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w,
             tc_fence_after();
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    abuf * C::kAccCols;
-            const int row = t.row0 + static_cast<int>(rank) * kTmRows + q * 32 + lane;
             tm_epilogue<GATE_UP, true, I8>(
-                p, tbase, row, row < t.row_end, t.i, (warp - 2) >> 2,
-                GATE_UP ? nullptr : epi_stage(g_tile + p.G + 1, warp), kTmN, nullptr,
-                t.g * p.w_group_rows + t.i * (GATE_UP ? kBM : kTmN));
+                p, tbase, row, row < t.row_end, t.i, half,
+                GATE_UP ? nullptr : epi_stage(g_tile + p.G + 1, warp), kTmN, nullptr, rs, scales);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(leader_tempty0 + abuf * 8);

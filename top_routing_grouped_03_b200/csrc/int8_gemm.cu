@@ -8,6 +8,10 @@
 // cores do twice the products (what bounds many tokens).  Tokens on M throughout: one-CTA
 // tiles of 128 tokens x 256 weight rows, K cut into slices when the tiles cannot fill the GPU,
 // and CTA pairs (256 x 256) once groups average 128 rows, as for bf16.
+//
+// gate_up leaves h in fp32: its row maxima are known only when all feature blocks are done.
+// (Letting the CTA that completes a row block quantise it, from L2, saved a launch but was bound
+// by the latency of one CTA's loads: 65536 x 1024 rows 436 -> 1640 us.)
 #include <algorithm>
 
 #include "grouped_gemm.cuh"
@@ -40,7 +44,7 @@ cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const Param
                              : static_cast<size_t>(CfgTm::kStages) * CfgTm::kStageBytes;
     const int stages = pair ? CfgPair::kStages : CfgTm::kStages;
     const size_t smem = 1024 + ring + (2 * stages + 5) * 8 + 16 + 2 * (p.G + 1) * sizeof(int) +
-                        (GATE_UP ? 0 : kEpiStageBytes);
+                        (GATE_UP ? 16 : kEpiStageBytes) + kScaleBytes;
     auto kfn = pair ? grouped_gemm_pair_kernel<GATE_UP, true> : grouped_gemm_tm_kernel<GATE_UP, true>;
     cudaError_t err = set_smem_limit(reinterpret_cast<const void*>(kfn), smem);
     if (err != cudaSuccess) return err;
@@ -70,12 +74,6 @@ cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const Param
 
 }  // namespace
 
-bool int8_gemm_uses_pairs(const Int8GemmLaunch& a, int num_sms) { return use_pairs(a, num_sms); }
-
-int int8_gemm_launches(const Int8GemmLaunch& a, int num_sms) {
-    if (a.rows == 0) return 0;
-    return a.kind == Int8GemmLaunch::kGateUp && a.sorted_token && use_pairs(a, num_sms) ? 2 : 1;
-}
 
 cudaError_t launch_int8_gemm(const Int8GemmLaunch& a, int num_sms, cudaStream_t s, bool pdl) {
     if (a.rows == 0) return cudaSuccess;

@@ -12,13 +12,16 @@
 // The selection is the one of the real numbers s_e, not of their fp32 roundings.  Without a
 // bias the logits themselves have the scores' order, so fp32 compares are exact (and a group
 // judged by its best expert too).  Otherwise the keys are computed in fp32, and where two
-// values that an output depends on come closer than the fp32 error bound below, the warp
-// repeats its token in fp64 (about one token in 500 of normally distributed logits).
+// values that an output depends on come closer than the fp32 error bound (`uncertain`), the
+// warp decides in fp64: between groups from all keys, between experts from the few that are
+// still in question.
 //
 // One warp per token, expert e = 32 j + lane in register j.  Keys are kept as unsigned
-// integers in the order of the floats, so that one redux.sync finds the best of a warp; a
-// second one finds the lowest index that has it.  Bound by issue: a round costs about 4 E / 32
-// instructions, the loads (4 E bytes a token) are a quarter of the time.
+// integers in the order of the floats.  TopK in two steps: the K-th best of the 32 lanes' own
+// maxima bounds the K-th best key from below; the keys that reach it (K to about 2 K of them)
+// are gathered, one to a lane, and each lane counts the ones before its own.  Counting against values broadcast from shared memory is a short chain of independent
+// compares; K rounds of warp-wide maxima were a chain of K times the latency (16381 x 256
+// logits, K = 8: 33 us).
 #include <algorithm>
 #include <cfloat>
 
@@ -34,8 +37,8 @@ constexpr unsigned kAll = 0xffffffffu;
 // Order-preserving map of floats (no NaN) to unsigned integers above 0; 0 is free for "not a
 // candidate".  -0 and +0 map alike.
 __device__ __forceinline__ uint32_t ordered(float v) {
-    const uint32_t b = __float_as_uint(v + 0.f);
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+    const int b = __float_as_int(v + 0.f);
+    return static_cast<uint32_t>(b ^ ((b >> 31) | static_cast<int>(0x80000000u)));
 }
 __device__ __forceinline__ float unordered(uint32_t u) {
     return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
@@ -47,7 +50,7 @@ __device__ __forceinline__ float load_logit(const bf16* p) {
 }
 
 // NaN -> -inf (out), +inf -> the largest finite number
-__device__ __forceinline__ float clean(float r) { return r == r ? fminf(r, FLT_MAX) : -INFINITY; }
+__device__ __forceinline__ float clean(float r) { return fminf(fmaxf(r, -INFINITY), FLT_MAX); }
 
 // The token's logit e: the sum of the planes (in order) and the logit bias, if any.
 template <typename T>
@@ -59,15 +62,16 @@ __device__ __forceinline__ float token_logit(const RouteLogitsLaunch& a, long lo
     return clean(r);
 }
 
-// The bound on the difference of two fp32 keys (or group scores) below which their order is
-// not certain.  With a bias: a sigmoid is off by at most 5e-7, a softmax by 2e-6 (expf and the
-// sum of 512 terms), the sum with the bias by 2^-24 of its size; a group score adds two of
-// them.  Without: softmax sums, whose common denominator does not matter, by 1.2e-5 of their
-// size for logits up to 100 below the largest (expf's argument is rounded); further
-// down they are tiny or 0 and compare as equal.
+// What two fp32 keys have to differ by for their order to be certain (twice this for scores
+// of groups, sums of two keys).  With a bias, per key: a sigmoid is off by at most 5e-7 (its
+// exponential's relative error counts s (1 - s) <= 1/4 times, and |r| s (1 - s) <= 0.23; a
+// reciprocal by 2 ulp), a softmax by 3e-6 (the same exponential and a sum of 512 terms), the sum
+// with the bias by 2^-24 of its size.  Without a bias only softmax sums are compared; their
+// common denominator does not matter, and a term is off by (|r - max| + 4) 2^-23 of its
+// size: 1.5e-5 for logits down to 100 below the largest, and what is smaller is 0.
 __device__ __forceinline__ float uncertain(const RouteLogitsLaunch& a, float size) {
-    if (a.select_bias == nullptr && a.score_mode == 0) return 3e-5f * fabsf(size);
-    return (a.score_mode == 0 ? 1.2e-5f : 4e-6f) + 1e-6f * fabsf(size);
+    if (a.select_bias == nullptr) return 1.5e-5f * fabsf(size);
+    return (a.score_mode == 0 ? 6e-6f : 1.3e-6f) + 2.5e-7f * fabsf(size);
 }
 
 template <typename V>
@@ -82,49 +86,71 @@ __device__ __forceinline__ V group_score(V m1, V m2, int group_top) {
     return group_top == 2 && m2 > -INFINITY ? m1 + m2 : m1;
 }
 
-// The token's selection in fp64, by one warp: idx of slot k into lane k.  key: E doubles of
-// this warp's shared memory.
-template <typename T>
-__device__ __noinline__ int select_fp64(const RouteLogitsLaunch& a, long long token, double* key,
-                                        int lane) {
-    const int E = a.E, S = E / a.n_group;
-    double m = -INFINITY, z = 0.;
-    if (a.score_mode == 0) {
-        for (int e = lane; e < E; e += 32) m = fmax(m, static_cast<double>(token_logit<T>(a, token, e)));
-        for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(kAll, m, o));
-        for (int e = lane; e < E; e += 32) {
-            const double r = token_logit<T>(a, token, e);
-            if (r > -INFINITY) z += exp(r - m);
-        }
-        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kAll, z, o);
+// The scores in fp64 (m, z: largest logit and sum of exponentials; softmax only).
+struct Exact {
+    double m, z;
+    __device__ __forceinline__ double score(const RouteLogitsLaunch& a, float r) const {
+        return a.score_mode == 0 ? exp(static_cast<double>(r) - m) / z
+                                 : 1. / (1. + exp(-static_cast<double>(r)));
     }
-    auto score = [&](double r) { return a.score_mode == 0 ? exp(r - m) / z : 1. / (1. + exp(-r)); };
-    // without a bias the logits order the experts, also where scores underflow
-    for (int e = lane; e < E; e += 32) {
-        double k = token_logit<T>(a, token, e);
-        if (a.select_bias && k > -INFINITY) {
-            k = score(k) + static_cast<double>(__ldg(a.select_bias + e));
-            if (!(k > -INFINITY)) k = -INFINITY;
+    // score + bias; -inf for an expert that is out
+    __device__ __forceinline__ double key(const RouteLogitsLaunch& a, float r, int e) const {
+        if (!(r > -INFINITY)) return -INFINITY;
+        double k = score(a, r);
+        if (a.select_bias) k += static_cast<double>(__ldg(a.select_bias + e));
+        return k > -INFINITY ? k : -INFINITY;
+    }
+    // the same order; without a bias the logits have it, also where scores underflow
+    __device__ __forceinline__ double order(const RouteLogitsLaunch& a, float r, int e) const {
+        return a.select_bias ? key(a, r, e) : static_cast<double>(r);
+    }
+};
+
+template <typename T>
+__device__ __noinline__ Exact exact_scores(const RouteLogitsLaunch& a, long long token, int lane) {
+    Exact x{-INFINITY, 0.};
+    if (a.score_mode == 0) {
+        for (int e = lane; e < a.E; e += 32) x.m = fmax(x.m, static_cast<double>(token_logit<T>(a, token, e)));
+        for (int o = 16; o > 0; o >>= 1) x.m = fmax(x.m, __shfl_xor_sync(kAll, x.m, o));
+#pragma unroll 4
+        for (int e = lane; e < a.E; e += 32) {
+            const float r = token_logit<T>(a, token, e);
+            if (r > -INFINITY) x.z += exp(static_cast<double>(r) - x.m);
         }
-        key[e] = k;
+        for (int o = 16; o > 0; o >>= 1) x.z += __shfl_xor_sync(kAll, x.z, o);
+    }
+    return x;
+}
+
+// The groups that stay (a bit each), in fp64.  key: E doubles of this warp's shared memory.
+template <typename T>
+__device__ __noinline__ unsigned exact_groups(const RouteLogitsLaunch& a, long long token,
+                                              double* key, int lane) {
+    const int S = a.E / a.n_group;
+    const Exact x = exact_scores<T>(a, token, lane);
+#pragma unroll 4
+    for (int e = lane; e < a.E; e += 32) key[e] = x.key(a, token_logit<T>(a, token, e), e);
+    __syncwarp();
+    double m1 = -INFINITY, m2 = -INFINITY;
+    if (lane < a.n_group)
+        for (int i = 0; i < S; ++i) keep_two(m1, m2, key[lane * S + i]);
+    const double mine = group_score(m1, m2, a.group_top);
+    int before = 0;  // groups ahead of this lane's
+    for (int g = 0; g < a.n_group; ++g) {
+        const double o = __shfl_sync(kAll, mine, g);
+        if (o > mine || (o == mine && g < lane)) ++before;
     }
     __syncwarp();
-    unsigned allowed = kAll;
-    if (a.topk_group < a.n_group) {
-        double m1 = -INFINITY, m2 = -INFINITY;
-        if (lane < a.n_group)
-            for (int i = 0; i < S; ++i) {
-                const double k = key[lane * S + i];
-                keep_two(m1, m2, a.select_bias == nullptr && k > -INFINITY ? score(k) : k);
-            }
-        const double mine = group_score(m1, m2, a.group_top);
-        int before = 0;  // groups ahead of this lane's
-        for (int g = 0; g < a.n_group; ++g) {
-            const double o = __shfl_sync(kAll, mine, g);
-            if (o > mine || (o == mine && g < lane)) ++before;
-        }
-        allowed = __ballot_sync(kAll, lane < a.n_group && before < a.topk_group);
-    }
+    return __ballot_sync(kAll, lane < a.n_group && before < a.topk_group);
+}
+
+// TopK in fp64 over every expert of the allowed groups: the expert of slot k into lane k.
+template <typename T>
+__device__ __noinline__ int exact_topk(const RouteLogitsLaunch& a, long long token, double* key,
+                                       unsigned allowed, int lane) {
+    const int E = a.E, S = E / a.n_group;
+    const Exact x = exact_scores<T>(a, token, lane);
+    for (int e = lane; e < E; e += 32) key[e] = x.order(a, token_logit<T>(a, token, e), e);
     unsigned taken = 0;  // of this lane's experts, by register j = e / 32
     int mine_k = 0;
     for (int k = 0; k < a.K; ++k) {
@@ -149,21 +175,128 @@ __device__ __noinline__ int select_fp64(const RouteLogitsLaunch& a, long long to
     return mine_k;
 }
 
-template <typename T, int NV>
-__device__ __forceinline__ void route_token(const RouteLogitsLaunch& a, long long token, float* sm,
-                                            int* hist, int lane) {
-    const int E = a.E, K = a.K, G = a.n_group, S = E / G;
-    const bool grouped = a.topk_group < G;
+// The K first of the lanes' candidates (e: expert; live: has one), by fp64 key:
+// the expert of slot k into lane k.
+template <typename T>
+__device__ __noinline__ int exact_order(const RouteLogitsLaunch& a, long long token, int e, bool live,
+                                        int lane) {
+    const Exact x = exact_scores<T>(a, token, lane);
+    const double k = live ? x.key(a, token_logit<T>(a, token, e), e) : -INFINITY;
+    int rank = 0;
+#pragma unroll 4
+    for (int l = 0; l < 32; ++l) {
+        const double o = __shfl_sync(kAll, k, l);
+        const int oe = __shfl_sync(kAll, live ? e : 0x7fffffff, l);
+        if (oe != 0x7fffffff && (o > k || (o == k && oe < e))) ++rank;
+    }
+    int mine = 0;
+    for (int s = 0; s < a.K; ++s) {
+        const int who = __ffs(__ballot_sync(kAll, live && rank == s)) - 1;
+        const int v = __shfl_sync(kAll, e, who);
+        if (lane == s) mine = v;
+    }
+    return mine;
+}
+
+// A key and the index that decides between equal ones (the lower first), as one number in the
+// order of the selection.
+__device__ __forceinline__ uint64_t with_index(uint32_t key, uint32_t index) {
+    return static_cast<uint64_t>(key) << 32 | (0xffffu - index);
+}
+__device__ __forceinline__ uint32_t index_of(uint64_t v) { return 0xffffu - static_cast<uint32_t>(v); }
+
+// How many of the n values in buf (shared memory, 16-byte aligned, followed by 0 where n is odd)
+// are larger than v.
+__device__ __forceinline__ int count_larger(const uint64_t* buf, int n, uint64_t v) {
+    int rank = 0;
+    for (int q = 0; q < n; q += 2) {
+        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(buf + q);
+        rank += (o.x > v) + (o.y > v);
+    }
+    return rank;
+}
+
+// The groups that stay (a bit each).  sm holds the values that groups are judged by, each group
+// of S padded to S + pad; lpg lanes look through a group.  best, next: scores of the last
+// group that stays and of the first that does not.
+__device__ __forceinline__ unsigned pick_groups(const RouteLogitsLaunch& a, uint32_t* sm, int S, int pad,
+                                                int lpg, uint32_t* best, uint32_t* next, int lane) {
+    const int g = lane >> (31 - __clz(lpg)), sub = lane & (lpg - 1);  // lpg: a power of two
+    uint32_t m1 = 0u, m2 = 0u;
+    if (g < a.n_group) {
+        const uint32_t* k = sm + g * (S + pad);
+        if ((S & 3) == 0) {
+            for (int i = 4 * sub; i < S; i += 4 * lpg) {
+                const uint4 v = *reinterpret_cast<const uint4*>(k + i);
+                const uint32_t hi = max(v.x, v.y), lo = min(v.x, v.y);
+                const uint32_t hj = max(v.z, v.w), lj = min(v.z, v.w);
+                const uint32_t h = max(hi, hj), l = max(min(hi, hj), hi > hj ? lo : lj);
+                m2 = max(max(min(m1, h), m2), l);
+                m1 = max(m1, h);
+            }
+        } else {
+            for (int i = sub; i < S; i += lpg) keep_two(m1, m2, k[i]);
+        }
+    }
+    for (int o = lpg >> 1; o > 0; o >>= 1) {
+        const uint32_t o1 = __shfl_xor_sync(kAll, m1, o), o2 = __shfl_xor_sync(kAll, m2, o);
+        m2 = max(min(m1, o1), max(m2, o2));
+        m1 = max(m1, o1);
+    }
+    const bool speaks = g < a.n_group && sub == 0;
+    uint32_t gs = m1;
+    if (a.group_top == 2 && speaks)
+        gs = ordered(group_score(unordered(m1), m2 ? unordered(m2) : -INFINITY, 2));
+    uint64_t* scores = reinterpret_cast<uint64_t*>(sm);
+    const uint64_t mine = with_index(gs, g);
+    __syncwarp();
+    if (speaks) scores[g] = mine;
+    if (lane == 0 && (a.n_group & 1)) scores[a.n_group] = 0u;
+    __syncwarp();
+    const bool stays = speaks && count_larger(scores, a.n_group, mine) < a.topk_group;
+    *best = __reduce_min_sync(kAll, stays ? gs : 0xffffffffu);
+    *next = __reduce_max_sync(kAll, speaks && !stays ? gs : 0u);
+    return __reduce_or_sync(kAll, stays ? 1u << g : 0u);
+}
+
+// Weights from differences of logits, for scores whose sum (nearly) underflows: there
+// sigma(r) = e^r to fp32 accuracy.
+__device__ __noinline__ float far_weight(float l) {
+    float best = l;
+    for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(kAll, best, o));
+    const float s = l > -INFINITY ? expf(l - best) : 0.f;
+    float sum = s;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    return sum > 0.f ? s / sum : 0.f;
+}
+
+// SUMS: the logits come in planes or with a bias.  The code is kept short (the rare paths are
+// calls): a launch of few tokens is bound by fetching it.
+template <typename T, int NV, bool SIGMOID, bool SUMS>
+__device__ __forceinline__ void route_token(const RouteLogitsLaunch& a, long long token,
+                                            uint32_t* sm, int* hist, int lane) {
+    const int E = a.E, K = a.K;
+    const bool grouped = a.topk_group < a.n_group;
     const bool on_logits = a.select_bias == nullptr;  // the logits have the keys' order
     const bool group_sums = grouped && a.group_top == 2;
+    const T* row = reinterpret_cast<const T*>(a.logits) + token * a.row_stride + lane;
     float r[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int e = j * 32 + lane;
-        r[j] = e < E ? token_logit<T>(a, token, e) : -INFINITY;
+    // (past E: out, and behind every real expert that is)
+    for (int j = 0; j < NV; ++j) r[j] = j * 32 + lane < E ? load_logit(row + j * 32) : -INFINITY;
+    if (SUMS) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (j * 32 + lane >= E) continue;
+            for (int q = 1; q < a.planes; ++q) r[j] += load_logit(row + j * 32 + q * a.plane_stride);
+            if (a.logit_bias) r[j] += __ldg(a.logit_bias + j * 32 + lane);
+        }
     }
-    float m = -INFINITY, z = 1.f;
-    if (a.score_mode == 0) {
+    float m = 0.f, z = 1.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) r[j] = clean(r[j]);
+    if (!SIGMOID) {
+        m = -INFINITY;
 #pragma unroll
         for (int j = 0; j < NV; ++j) m = fmaxf(m, r[j]);
         m = unordered(__reduce_max_sync(kAll, ordered(m)));
@@ -171,137 +304,174 @@ __device__ __forceinline__ void route_token(const RouteLogitsLaunch& a, long lon
         if (!on_logits || !a.renorm) {
             z = 0.f;
 #pragma unroll
-            for (int j = 0; j < NV; ++j) z += expf(r[j] - m);
+            for (int j = 0; j < NV; ++j) z += __expf(r[j] - m);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kAll, z, o);
             if (z == 0.f) z = 1.f;
         }
     }
-    auto score = [&](float v) { return a.score_mode == 0 ? expf(v - m) / z : 1.f / (1.f + expf(-v)); };
     uint32_t key[NV];
-    bool sure = true;
-    const int lpg = 32 / a.group_lanes;  // lanes that share a group's keys
+    if (on_logits && !group_sums) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int e = j * 32 + lane;
-        key[j] = 0u;
-        if (e < E) {
-            float k = r[j], in_group = r[j];
-            if (!on_logits) {
-                k = r[j] > -INFINITY ? score(r[j]) + __ldg(a.select_bias + e) : -INFINITY;
-                in_group = k = k > -INFINITY ? k : -INFINITY;
-            } else if (group_sums) {
-                in_group = r[j] > -INFINITY ? score(r[j]) : -INFINITY;
-            }
-            key[j] = ordered(k);
-            if (grouped) sm[e + ((e * a.group_magic) >> 20) * lpg] = in_group;
-        }
-    }
-    if (grouped) {
-        __syncwarp();
-        const int g = lane / lpg, sub = lane % lpg;
-        float m1 = -INFINITY, m2 = -INFINITY;
-        if (g < G)
-            for (int i = sub; i < S; i += lpg) keep_two(m1, m2, sm[g * (S + lpg) + i]);
-        for (int o = lpg >> 1; o > 0; o >>= 1) {
-            const float o1 = __shfl_xor_sync(kAll, m1, o), o2 = __shfl_xor_sync(kAll, m2, o);
-            keep_two(m1, m2, o1);
-            keep_two(m1, m2, o2);
-        }
-        __syncwarp();
-        uint32_t gs = g < G && sub == 0 ? ordered(group_score(m1, m2, a.group_top)) : 0u;
-        unsigned allowed = 0;
-        uint32_t best = 0;
-        for (int i = 0; i < a.topk_group; ++i) {
-            best = __reduce_max_sync(kAll, gs);
-            const int who = __ffs(__ballot_sync(kAll, gs == best)) - 1;  // the lowest group
-            allowed |= 1u << (who / lpg);
-            if (lane == who) gs = 0u;
-        }
-        if (!on_logits || group_sums) {
-            const float last = unordered(best), next = unordered(__reduce_max_sync(kAll, gs));
-            if (next > -INFINITY && !(last - next > uncertain(a, last))) sure = false;
-        }
+        for (int j = 0; j < NV; ++j) key[j] = ordered(r[j]);
+    } else {
+        // scores for comparing (the weights below are computed with expf and divisions)
+        const float inv_z = __fdividef(1.f, z);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int e = j * 32 + lane;
-            if (!((allowed >> ((e * a.group_magic) >> 20)) & 1u)) key[j] = 0u;
+            float k = SIGMOID ? __fdividef(1.f, 1.f + __expf(-r[j])) : __expf(r[j] - m) * inv_z;
+            if (!on_logits && e < E) k += __ldg(a.select_bias + e);
+            key[j] = ordered(r[j] > -INFINITY ? fmaxf(k, -INFINITY) : -INFINITY);
         }
     }
+    unsigned allowed = kAll;
+    if (grouped) {
+        const int S = E / a.n_group, lpg = 32 / a.group_lanes;
+        const int pad = (S & 3) == 0 ? 4 * lpg : lpg;  // keeps the lanes' reads off each other's banks
+        if (a.whole_registers) {  // groups of 32 m experts: one group to a register
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (j * 32 < E) sm[j * 32 + ((j * 32 * a.group_magic) >> 20) * pad + lane] = key[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int e = j * 32 + lane;
+                if (e < E) sm[e + ((e * a.group_magic) >> 20) * pad] = key[j];
+            }
+        }
+        __syncwarp();
+        uint32_t best, next;
+        allowed = pick_groups(a, sm, S, pad, lpg, &best, &next, lane);
+        if (!on_logits || group_sums) {
+            const float last = unordered(best), after = unordered(next);
+            if (after > -INFINITY && !(last - after > 2.f * uncertain(a, last)))
+                allowed = exact_groups<T>(a, token, reinterpret_cast<double*>(sm), lane);
+        }
+        if (on_logits && group_sums) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) key[j] = ordered(r[j]);
+        }
+        if (a.whole_registers) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (!((allowed >> ((j * 32 * a.group_magic) >> 20)) & 1u)) key[j] = 0u;
+        } else {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int e = j * 32 + lane;  // (past E: 0, the group may not exist)
+                if (e >= E || !((allowed >> ((e * a.group_magic) >> 20)) & 1u)) key[j] = 0u;
+            }
+        }
+    }
+    // A lower bound of the K-th best key: the K-th best of the lanes' maxima (0: fewer lanes than
+    // K have a candidate, so every candidate counts).
+    uint32_t top = 0u;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) top = max(top, key[j]);
+    __syncwarp();
+    sm[lane] = top;
+    __syncwarp();
+    int above = 0;
+#pragma unroll
+    for (int q = 0; q < 32; q += 4) {
+        const uint4 o = *reinterpret_cast<const uint4*>(sm + q);
+        above += (o.x > top) + (o.y > top) + (o.z > top) + (o.w > top);
+    }
+    const uint32_t bound = __reduce_min_sync(kAll, above < K ? top : 0xffffffffu);
+    // what may still come before an expert at the bound in real numbers
+    uint32_t low = max(bound, 1u);
+    if (!on_logits && bound) {
+        const float v = unordered(bound);
+        if (v > -INFINITY) low = ordered(v - uncertain(a, v));
+    }
+    // candidates to shared memory, lane by lane
+    uint64_t* cand = reinterpret_cast<uint64_t*>(sm);
+    int own = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) own += key[j] >= low;
+    int at = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kAll, at, o);
+        if (lane >= o) at += v;
+    }
+    const int n = __shfl_sync(kAll, at, 31);
     int my_e = 0;
-    float prev = INFINITY;
-    for (int k = 0; k < K; ++k) {
-        uint32_t b = 0u;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) b = max(b, key[j]);
-        b = __reduce_max_sync(kAll, b);
-        int e = 0x7fffffff;
-#pragma unroll
-        for (int j = NV - 1; j >= 0; --j)
-            if (key[j] == b) e = j * 32 + lane;
-        e = __reduce_min_sync(kAll, static_cast<unsigned>(e));
+    float l = -INFINITY;  // the slot's logit
+    if (n <= 32) {
+        at -= own;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (j * 32 + lane == e) key[j] = 0u;
-        if (lane == k) my_e = e;
-        const float v = unordered(b);
-        if (!on_logits && v > -INFINITY && !(prev - v > uncertain(a, v))) sure = false;
-        prev = v;
+            if (key[j] >= low) cand[at++] = with_index(key[j], j * 32 + lane);
+        if (lane == 0) cand[n] = 0u;
+        __syncwarp();
+        const uint64_t mine = cand[lane];
+        const int rank = lane < n ? count_larger(cand, n, mine) : 32;
+        uint64_t* slot = cand + 34;  // K + 1 places
+        if (lane == K) slot[K] = 0u;
+        __syncwarp();
+        if (rank <= K) slot[rank] = mine;
+        __syncwarp();
+        bool sure = true;
+        if (lane < K) {
+            const uint32_t k = static_cast<uint32_t>(slot[lane] >> 32);
+            my_e = static_cast<int>(index_of(slot[lane]));
+            if (on_logits) {
+                l = unordered(k);
+            } else {
+                l = token_logit<T>(a, token, my_e);
+                const uint32_t after = static_cast<uint32_t>(slot[lane + 1] >> 32);
+                const float v = unordered(k), va = after ? unordered(after) : -INFINITY;
+                sure = va == -INFINITY || v - va > uncertain(a, v);
+            }
+        }
+        if (!__all_sync(kAll, sure)) {
+            const int e = static_cast<int>(index_of(mine));
+            my_e = exact_order<T>(a, token, e, lane < n && e < E, lane);
+            if (lane < K) l = token_logit<T>(a, token, my_e);
+        }
+    } else {
+        // many keys that (nearly) equal the bound
+        my_e = exact_topk<T>(a, token, reinterpret_cast<double*>(sm), allowed, lane);
+        if (lane < K) l = token_logit<T>(a, token, my_e);
     }
-    if (!on_logits) {  // the best one left out
-        uint32_t b = 0u;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) b = max(b, key[j]);
-        b = __reduce_max_sync(kAll, b);
-        const float v = b ? unordered(b) : -INFINITY;
-        if (v > -INFINITY && !(prev - v > uncertain(a, v))) sure = false;
-    }
-    if (!sure) my_e = select_fp64<T>(a, token, reinterpret_cast<double*>(sm), lane);
     // weights: the selected scores, in the lanes of their slots
-    float s = 0.f, l = -INFINITY;
+    float w = 0.f;
     if (lane < K) {
-        l = token_logit<T>(a, token, my_e);
-        if (a.select_bias && l > -INFINITY && !(score(l) + __ldg(a.select_bias + my_e) > -INFINITY))
+        w = SIGMOID ? 1.f / (1.f + expf(-l)) : expf(l - m) / z;
+        if (!(l > -INFINITY) || (a.select_bias && !(w + __ldg(a.select_bias + my_e) > -INFINITY))) {
             l = -INFINITY;
-        s = l > -INFINITY ? score(l) : 0.f;
+            w = 0.f;
+        }
     }
     if (a.renorm) {
-        float sum = s;
+        float sum = w;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-        if (sum < 1e-30f) {
-            // scores that (nearly) underflow: the same ratios from differences of logits, in
-            // which sigma(r) = e^r to fp32 accuracy this far down
-            float top = l;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-            s = l > -INFINITY ? expf(l - top) : 0.f;
-            sum = s;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-        }
-        s = sum > 0.f ? s / sum : 0.f;
+        w = sum < 1e-30f ? far_weight(l) : w / sum;
     }
     if (lane < K) {
         a.topk_idx[token * K + lane] = my_e;
-        a.topk_w[token * K + lane] = s * a.scale;
+        a.topk_w[token * K + lane] = w * a.scale;
         if (a.counts) atomicAdd(hist + my_e, 1);
     }
 }
 
-template <typename T, int NV>
-__global__ void __launch_bounds__(kThreads) route_logits_kernel(const __grid_constant__ RouteLogitsLaunch a, int warp_bytes) {
+template <typename T, int NV, bool SIGMOID, bool SUMS>
+__global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 3)
+route_logits_kernel(const __grid_constant__ RouteLogitsLaunch a, int warp_bytes) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int hist[512];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float* sm = reinterpret_cast<float*>(smem + static_cast<size_t>(warp) * warp_bytes);
+    uint32_t* sm = reinterpret_cast<uint32_t*>(smem + static_cast<size_t>(warp) * warp_bytes);
     for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
     __syncthreads();
     grid_dep_wait();
     grid_dep_launch();
     for (long long t = static_cast<long long>(blockIdx.x) * kWarps + warp; t < a.T;
          t += static_cast<long long>(gridDim.x) * kWarps)
-        route_token<T, NV>(a, t, sm, hist, lane);
+        route_token<T, NV, SIGMOID, SUMS>(a, t, sm, hist, lane);
     __syncthreads();
     if (a.counts)
         for (int e = threadIdx.x; e < a.E; e += kThreads) {
@@ -310,7 +480,7 @@ __global__ void __launch_bounds__(kThreads) route_logits_kernel(const __grid_con
         }
 }
 
-template <typename T>
+template <typename T, bool SIGMOID, bool SUMS>
 cudaError_t launch_typed(const RouteLogitsLaunch& a, int grid, size_t warp_bytes, cudaStream_t s,
                          bool pdl) {
     const int nv = ceil_div(a.E, 32);
@@ -319,11 +489,11 @@ cudaError_t launch_typed(const RouteLogitsLaunch& a, int grid, size_t warp_bytes
         return launch_kernel(kernel, dim3(grid), dim3(kThreads), smem, s, pdl, a,
                              static_cast<int>(warp_bytes));
     };
-    return nv <= 1   ? go(route_logits_kernel<T, 1>)
-           : nv <= 2 ? go(route_logits_kernel<T, 2>)
-           : nv <= 4 ? go(route_logits_kernel<T, 4>)
-           : nv <= 8 ? go(route_logits_kernel<T, 8>)
-                     : go(route_logits_kernel<T, 16>);
+    return nv <= 1   ? go(route_logits_kernel<T, 1, SIGMOID, SUMS>)
+           : nv <= 2 ? go(route_logits_kernel<T, 2, SIGMOID, SUMS>)
+           : nv <= 4 ? go(route_logits_kernel<T, 4, SIGMOID, SUMS>)
+           : nv <= 8 ? go(route_logits_kernel<T, 8, SIGMOID, SUMS>)
+                     : go(route_logits_kernel<T, 16, SIGMOID, SUMS>);
 }
 
 }  // namespace
@@ -341,17 +511,25 @@ cudaError_t launch_route_logits(const RouteLogitsLaunch& in, int num_sms, cudaSt
     const int S = a.E / a.n_group;
     a.group_lanes = 1;
     while (a.group_lanes < a.n_group) a.group_lanes *= 2;
+    a.whole_registers = S % 32 == 0;
     a.group_magic = ((1 << 20) + S - 1) / S;  // e / S = e * magic >> 20 for e < 512
-    // a warp's keys by group (each group padded against bank conflicts), or its fp64 keys
-    const size_t padded = sizeof(float) * (a.E + static_cast<size_t>(a.n_group) * (32 / a.group_lanes));
-    size_t warp_bytes = 0;
-    if (a.select_bias || (a.topk_group < a.n_group && a.group_top == 2))
-        warp_bytes = sizeof(double) * a.E;
-    if (a.topk_group < a.n_group && warp_bytes < padded) warp_bytes = padded;
+    // a warp's shared memory: the keys by group, each group padded; candidates and slots; the
+    // fp64 keys of the rare paths
+    const int lpg = 32 / a.group_lanes;
+    size_t warp_bytes = std::max<size_t>(sizeof(uint64_t) * (34 + 18), sizeof(double) * a.E);
+    if (a.topk_group < a.n_group)
+        warp_bytes = std::max(warp_bytes, sizeof(uint32_t) * (a.E + static_cast<size_t>(a.n_group) * 4 * lpg));
     warp_bytes = (warp_bytes + 15) & ~static_cast<size_t>(15);
     const int grid = one ? 1 : static_cast<int>(std::min<long long>(ceil_div(a.T, kWarps), 4ll * num_sms));
-    const cudaError_t err = a.is_bf16 ? launch_typed<bf16>(a, grid, warp_bytes, s, pdl)
-                                      : launch_typed<float>(a, grid, warp_bytes, s, pdl);
+    // (bf16 logits are given ones: no planes, no bias)
+    const bool sums = a.planes > 1 || a.logit_bias != nullptr, sigmoid = a.score_mode != 0;
+    const cudaError_t err =
+        a.is_bf16 ? (sigmoid ? launch_typed<bf16, true, false>(a, grid, warp_bytes, s, pdl)
+                             : launch_typed<bf16, false, false>(a, grid, warp_bytes, s, pdl))
+        : sums    ? (sigmoid ? launch_typed<float, true, true>(a, grid, warp_bytes, s, pdl)
+                             : launch_typed<float, false, true>(a, grid, warp_bytes, s, pdl))
+                  : (sigmoid ? launch_typed<float, true, false>(a, grid, warp_bytes, s, pdl)
+                             : launch_typed<float, false, false>(a, grid, warp_bytes, s, pdl));
     count_launches(1);
     return err;
 }
