@@ -308,6 +308,7 @@ def _need(ok: bool, what: str):
         raise MoEError(-1, what)
 
 
+_empty = torch.empty_strided  # (the call that costs the host least)
 _get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
@@ -370,9 +371,10 @@ def route_logits(logits, K, score="softmax", select_bias=None, n_group=1, topk_g
     if select_bias is not None:
         _q(select_bias, F32, dev)
     x = _q(logits, F32 if kind == 0 else BF16, dev)
-    idx = logits.new_empty((T, K), dtype=I32)
-    w = logits.new_empty((T, K), dtype=F32)
-    counts = logits.new_empty((E,), dtype=I32)
+    device = logits.device
+    idx = _empty((T, K), (K, 1), dtype=I32, device=device)
+    w = _empty((T, K), (K, 1), dtype=F32, device=device)
+    counts = _empty((E,), (1,), dtype=I32, device=device)
     _check(lib().moe_route_logits(x, kind, T, E, K, rule, idx.data_ptr(), w.data_ptr(),
                                   counts.data_ptr(), _raw_stream(dev)), "moe_route_logits")
     return idx, w, counts
@@ -385,9 +387,10 @@ def quantize_rows(x):
     _need(x.dim() >= 1, "quantize_rows (x must have rows)")
     dev = x.get_device()
     p = _q(x, BF16, dev)
-    q = x.new_empty(x.shape, dtype=I8)
-    scale = x.new_empty(x.shape[:-1], dtype=F32)
-    _check(lib().moe_quantize_rows(p, scale.numel(), x.shape[-1], q.data_ptr(), scale.data_ptr(),
+    shape = x.shape
+    q = _empty(shape, x.stride(), dtype=I8, device=x.device)  # (x is contiguous)
+    scale = torch.empty(shape[:-1], dtype=F32, device=x.device)
+    _check(lib().moe_quantize_rows(p, scale.numel(), shape[-1], q.data_ptr(), scale.data_ptr(),
                                    _raw_stream(dev)), "moe_quantize_rows")
     return q, scale
 
@@ -397,10 +400,12 @@ def _int8_buffers(x, T, N, K, out, workspace):
     if n == 0:
         raise MoEError(-2, "moe_int8_workspace_size")
     if out is None:
-        out = x.new_empty((T, N), dtype=BF16)
+        out = _empty((T, N), (N, 1), dtype=BF16, device=x.device)
     else:
         _need(out.shape == (T, N), "int8 product (out must be [T, N])")
-    return out, x.new_empty((n,), dtype=U8) if workspace is None else workspace
+    if workspace is None:
+        workspace = _empty((n,), (1,), dtype=U8, device=x.device)
+    return out, workspace
 
 
 @_on_device_of
@@ -467,9 +472,9 @@ def experts_int8(xq, x_scale, topk_w, perm, w_gate_up, gate_up_scale, w_down, do
         n = int(lib().moe_experts_int8_workspace_size(T, D, E, K, f, flags))
         if n == 0:
             raise MoEError(-2, "moe_experts_int8_workspace_size")
-        workspace = xq.new_empty((n,), dtype=U8)
+        workspace = _empty((n,), (1,), dtype=U8, device=xq.device)
     if out is None:
-        out = xq.new_empty((T, D), dtype=BF16)
+        out = _empty((T, D), (D, 1), dtype=BF16, device=xq.device)
     _check(lib().moe_experts_int8(prm, _q(out, BF16, dev), _q(workspace, U8, dev),
                                   workspace.numel(), _raw_stream(dev)), "moe_experts_int8")
     return out

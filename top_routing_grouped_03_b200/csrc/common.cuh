@@ -265,6 +265,31 @@ struct Int8GemmLaunch {
 };
 cudaError_t launch_int8_gemm(const Int8GemmLaunch& a, int num_sms, cudaStream_t s, bool pdl);
 
+// The same for a handful of tokens, on the CUDA cores (int8_few.cu).  x != NULL: the tokens are
+// quantised in the kernel; otherwise xq and x_scale are given.
+bool few_linear_ok(int T, int K);
+cudaError_t launch_few_linear(const bf16* x, const int8_t* xq, const float* x_scale, const int8_t* w,
+                              const float* w_scale, int T, int N, int K, bf16* out, int num_sms,
+                              cudaStream_t s);
+constexpr int kFewRows = 16;  // (token, expert) rows
+struct Int8FewExperts {
+    const int8_t* xq;
+    const float* x_scale;
+    const int32_t* offsets;
+    const int32_t* sorted_token;
+    const float* sorted_w;
+    const int8_t* w_gate_up;
+    const float* gate_up_scale;
+    const int8_t* w_down;
+    const float* down_scale;
+    const bf16* residual;  // or NULL
+    int T, D, E, K, f;
+    float* h;              // [T*K, f]
+    bf16* out;
+};
+bool few_experts_ok(int T, int D, int K, int f);
+cudaError_t launch_few_experts(const Int8FewExperts& a, int num_sms, cudaStream_t s);
+
 // expert parallelism (ep.cu): receive-side grouping and the return of the expert rows
 size_t ep_recv_layout_smem(int G, int El);
 cudaError_t launch_ep_recv_layout(const int32_t* recv_counts, int G, int El, int n,

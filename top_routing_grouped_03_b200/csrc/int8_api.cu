@@ -184,6 +184,25 @@ cudaError_t run_experts(const moe_int8_experts& p, const ExpertsLayout& L, void*
     return launch_int8_gemm(dn, sms, s, true);
 }
 
+// The whole of moe_experts_int8 for a handful of rows: two launches.
+cudaError_t run_few(const moe_int8_experts& p, float* h, moe_bf16* out, int sms, cudaStream_t s) {
+    Int8FewExperts a{};
+    a.xq = p.xq;
+    a.x_scale = p.x_scale;
+    a.offsets = p.expert_offsets;
+    a.sorted_token = p.sorted_token;
+    a.sorted_w = p.sorted_w;
+    a.w_gate_up = p.w_gate_up;
+    a.gate_up_scale = p.gate_up_scale;
+    a.w_down = p.w_down;
+    a.down_scale = p.down_scale;
+    a.residual = reinterpret_cast<const bf16*>(p.residual);
+    a.T = p.T; a.D = p.D; a.E = p.E; a.K = p.K; a.f = p.f;
+    a.h = h;
+    a.out = reinterpret_cast<bf16*>(out);
+    return launch_few_experts(a, sms, s);
+}
+
 int check_experts_shape(int T, int D, int E, int K, int f) {
     const int rc = check_shape(T, D, E, K, f, 0);
     if (rc) return rc;
@@ -317,7 +336,10 @@ int layer_int8(const moe_layer_params* p, const RouteLogitsLaunch* rule, const m
     e.gate_up_scale = w->gate_up_scale;
     e.w_down = w->down;
     e.down_scale = w->down_scale;
+    e.residual = p->residual;
     e.T = T; e.D = D; e.E = E; e.K = K; e.f = f;
+    if (!shared && few_experts_ok(T, D, K, f))
+        return run_few(e, at<float>(ws, L.x.h), out, sms, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     float* acc = at<float>(ws, L.x.acc);
     float* y = det ? at<float>(ws, L.x.y) : nullptr;
     if (det && shared &&
@@ -464,6 +486,11 @@ int moe_int8_matmul(const int8_t* xq, const float* x_scale, const int8_t* wq, co
     if ((reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0) return MOE_ERR_ALIGN;
     if (T == 0) return MOE_OK;
     cudaStream_t s = as_stream(stream);
+    if (few_linear_ok(T, K))
+        return launch_few_linear(nullptr, xq, x_scale, wq, w_scale, T, N, K,
+                                 reinterpret_cast<bf16*>(out), num_sms_current(), s) == cudaSuccess
+                   ? MOE_OK
+                   : MOE_ERR_CUDA;
     if (cudaMemsetAsync(workspace, 0, 4ull * L.clear_words, s) != cudaSuccess) return MOE_ERR_CUDA;
     return launch_dense(xq, x_scale, wq, w_scale, T, N, K, out, workspace, L, s, false) == cudaSuccess
                ? MOE_OK
@@ -481,6 +508,11 @@ int moe_int8_linear(const moe_bf16* x, const int8_t* wq, const float* w_scale, i
     if ((reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0) return MOE_ERR_ALIGN;
     if (T == 0) return MOE_OK;
     cudaStream_t s = as_stream(stream);
+    if (few_linear_ok(T, K))
+        return launch_few_linear(reinterpret_cast<const bf16*>(x), nullptr, nullptr, wq, w_scale, T, N,
+                                 K, reinterpret_cast<bf16*>(out), num_sms_current(), s) == cudaSuccess
+                   ? MOE_OK
+                   : MOE_ERR_CUDA;
     QuantizeLaunch q{};
     q.x = x;
     q.rows = T;
@@ -519,6 +551,8 @@ int moe_experts_int8(const moe_int8_experts* p, moe_bf16* out, void* workspace, 
     if (T == 0) return MOE_OK;
     cudaStream_t s = as_stream(stream);
     const int sms = num_sms_current();
+    if (few_experts_ok(T, D, K, f))
+        return run_few(*p, at<float>(workspace, L.h), out, sms, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     if (cudaMemsetAsync(workspace, 0, L.zero_end, s) != cudaSuccess) return MOE_ERR_CUDA;
     float* acc = det ? nullptr : at<float>(workspace, L.acc);
     float* y = det ? at<float>(workspace, L.y) : nullptr;
