@@ -130,7 +130,7 @@ cudaError_t launch_tpl(const CUtensorMap& mw, const CUtensorMap& ma, const Param
 template <bool GATE_UP>
 cudaError_t launch_tm(const CUtensorMap& mw, const CUtensorMap& ma, const Params& p, int grid,
                       cudaStream_t s, bool pdl) {
-    using C = CfgTm;
+    using C = CfgTm<>;
     const size_t smem = 1024 + static_cast<size_t>(C::kStages) * C::kStageBytes +
                         (2 * C::kStages + 5) * 8 + 16 + 2 * (p.G + 1) * sizeof(int) +
                         (GATE_UP ? 0 : kEpiStageBytes);

@@ -802,38 +802,41 @@ __device__ __forceinline__ float row_scale_of(const Params& p, int row) {
 }
 
 // The column scales of a warp's share of a tile into its 128 floats of shared memory: gate_up
-// 64 gate and 64 up features, otherwise 128 output columns.  Issued before the wait for the
-// accumulator, so that the loads (weights' scales come from HBM) overlap the products.
+// WN / 4 gate and as many up features, otherwise WN / 2 output columns.  Issued before the
+// wait for the accumulator, so that the loads (weights' scales come from HBM) overlap the
+// products.
 constexpr int kScaleFloats = 128;
-template <bool GATE_UP>
+template <bool GATE_UP, int WN>
 __device__ __forceinline__ void stage_scales(const Params& p, float* dst, int wr, int col0, int half,
                                              int lane) {
+    constexpr int kLanes = WN / 8;  // lanes that load four scales each
     const float* src;
-    bool in = true;
+    bool in = lane < kLanes;
     if (GATE_UP) {
-        src = p.col_scale + wr + half * 64 + (lane < 16 ? 4 * lane : p.up_rows + 4 * (lane - 16));
+        src = p.col_scale + wr + half * (WN / 4) +
+              (lane < kLanes / 2 ? 4 * lane : p.up_rows + 4 * (lane - kLanes / 2));
     } else {
-        src = p.col_scale + wr + half * 128 + 4 * lane;
-        in = col0 + half * 128 + 4 * lane < p.out_cols;
+        src = p.col_scale + wr + half * (WN / 2) + 4 * lane;
+        in = in && col0 + half * (WN / 2) + 4 * lane < p.out_cols;
     }
     __syncwarp();  // the last tile's reads are over
     if (in) *reinterpret_cast<float4*>(dst + 4 * lane) = __ldg(reinterpret_cast<const float4*>(src));
     __syncwarp();
 }
 
-// gate_up: h (fp32) of the warp's 32 rows x 64 features from feature feat on; rs: the row's scale.
+// gate_up: h (fp32) of the warp's 32 rows x hc features from feature feat on; rs: the row's scale.
 __device__ __forceinline__ void i8_gate_up_epilogue(const Params& p, uint32_t tgate, uint32_t tup,
-                                                    int row, bool valid, float rs, int feat,
+                                                    int row, bool valid, float rs, int feat, int hc,
                                                     const float* scales) {
     float* hrow = p.h32_out + static_cast<size_t>(row) * p.out_cols + feat;
 #pragma unroll 1
-    for (int c0 = 0; c0 < 64; c0 += 16) {
+    for (int c0 = 0; c0 < hc; c0 += 16) {
         uint32_t gv[16], uv[16];
         tmem_ld16(tgate + c0, gv);
         tmem_ld16(tup + c0, uv);
         tmem_ld_wait();
         scale_columns<16>(gv, scales + c0);
-        scale_columns<16>(uv, scales + 64 + c0);
+        scale_columns<16>(uv, scales + hc + c0);
         if (valid) {
             float4* dst = reinterpret_cast<float4*>(hrow + c0);
 #pragma unroll
@@ -960,7 +963,7 @@ __device__ __forceinline__ void tm_epilogue(const Params& p, uint32_t tbase, int
             i8_store_partials(tbase + F + half * hc, prow + p.out_cols, hc, valid);
         } else {
             i8_gate_up_epilogue(p, tbase + half * hc, tbase + F + half * hc, row, valid, rs, feat,
-                                scales);
+                                hc, scales);
         }
     } else if (I8 && p.dense) {
         // dense product; the last tile may hold fewer than wn columns
@@ -1128,22 +1131,25 @@ __device__ __forceinline__ float i8_row_scale(const Params& p, int row) {
     return s;
 }
 
+// WN: weight rows of a tile (256; the int8 kernels also 128 and 64, see int8_gemm.cu).
+template <int WN = kTmN>
 struct CfgTm {
     static constexpr int kABytes = kTmRows * kBK * 2;  // 16 KB of token rows
-    static constexpr int kBBytes = kTmN * kBK * 2;     // 32 KB of weight rows
+    static constexpr int kBBytes = WN * kBK * 2;       // 32 KB of weight rows at 256
     static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kStages = 4;
-    static constexpr int kAccCols = kTmN;
+    static constexpr int kStages = 192 * 1024 / kStageBytes;  // 4 at 256
+    static constexpr int kAccCols = WN;
     static constexpr int kTmemCols = 2 * kAccCols;
+    static_assert(WN == 256 || WN == 128 || WN == 64, "TMA boxes of WN / 2 rows");
     static_assert(kTmemCols <= 512, "accumulators exceed tensor memory");
 };
 
 // I8: 8-bit operands (the K step of 64 pairs is 128 values, one MMA per 32 of them).
-template <bool GATE_UP, bool I8 = false>
+template <bool GATE_UP, bool I8 = false, int WN = kTmN>
 __global__ void __launch_bounds__(kTmThreads, 1)
 grouped_gemm_tm_kernel(const __grid_constant__ CUtensorMap map_w,
                        const __grid_constant__ CUtensorMap map_act, Params p) {
-    using C = CfgTm;
+    using C = CfgTm<WN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -1211,8 +1217,8 @@ grouped_gemm_tm_kernel(const __grid_constant__ CUtensorMap map_w,
                 const int ke = slice_begin(p.nk, un.nsl, un.slice + 1);
                 // gate_up: gate rows g*2f + i*128 and up rows g*2f + f + i*128;
                 // down: rows g*D + i*256 and the next 128
-                const int wr0 = t.g * p.w_group_rows + t.i * (GATE_UP ? kBM : kTmN);
-                const int wr1 = GATE_UP ? wr0 + p.up_rows : wr0 + kBM;
+                const int wr0 = t.g * p.w_group_rows + t.i * (GATE_UP ? WN / 2 : WN);
+                const int wr1 = GATE_UP ? wr0 + p.up_rows : wr0 + WN / 2;
                 RowGather<kTmRows> rg;
                 if (gather) rg.plan(p.gather_tok, t.row0, t.row_end, p.nk * kBK, lane);
                 for (int kk = kb; kk < ke; ++kk) {
@@ -1230,7 +1236,7 @@ grouped_gemm_tm_kernel(const __grid_constant__ CUtensorMap map_w,
                         if (!gather)
                             tma_load_2d(st, &map_act, &full[stage], kk * kBK, t.row0, pol_a);
                         tma_load_2d(st + C::kABytes, &map_w, &full[stage], kk * kBK, wr0, pol_w);
-                        tma_load_2d(st + C::kABytes + kBM * kBK * 2, &map_w, &full[stage],
+                        tma_load_2d(st + C::kABytes + C::kBBytes / 2, &map_w, &full[stage],
                                     kk * kBK, wr1, pol_w);
                     }
                     if (gather) {
@@ -1253,7 +1259,7 @@ grouped_gemm_tm_kernel(const __grid_constant__ CUtensorMap map_w,
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
         if (lane == 0) {
-            constexpr uint32_t idesc = I8 ? idesc_i8_s32(kTmRows, kTmN) : idesc_bf16_f32(kTmRows, kTmN);
+            constexpr uint32_t idesc = I8 ? idesc_i8_s32(kTmRows, WN) : idesc_bf16_f32(kTmRows, WN);
             int stage = 0;
             uint32_t phase = 0, abuf = 0, aphase = 0;
             bool ok = true, issued = false;
@@ -1314,11 +1320,11 @@ grouped_gemm_tm_kernel(const __grid_constant__ CUtensorMap map_w,
             const int row = t.row0 + q * 32 + lane;
             const bool valid = row < t.row_end;
             const int half = (warp - 2) >> 2;
-            const int wr = t.g * p.w_group_rows + t.i * (GATE_UP ? kBM : kTmN);
+            const int wr = t.g * p.w_group_rows + t.i * (GATE_UP ? WN / 2 : WN);
             float rs = 1.f;
             if (I8) {
                 rs = valid ? i8_row_scale<GATE_UP>(p, row) : 0.f;
-                stage_scales<GATE_UP>(p, scales, wr, t.i * kTmN, half, lane);
+                stage_scales<GATE_UP, WN>(p, scales, wr, t.i * WN, half, lane);
             }
             const bool ready = mbar_wait(&tfull[abuf], aphase, kWaitBudgetNs, abort_flag);
             if (!epilogue_bar_and<kTmEpiThreads>(ready)) {
@@ -1338,7 +1344,7 @@ grouped_gemm_tm_kernel(const __grid_constant__ CUtensorMap map_w,
                               : nullptr;
             tm_epilogue<GATE_UP, false, I8>(
                 p, tbase, row, valid, t.i, half,
-                GATE_UP ? nullptr : epi_stage(g_tile + p.G + 1, warp), kTmN, part, rs, scales);
+                GATE_UP ? nullptr : epi_stage(g_tile + p.G + 1, warp), WN, part, rs, scales);
             tc_fence_before();
             mbar_arrive(&tempty[abuf]);
             abuf ^= 1u;
@@ -1347,7 +1353,7 @@ grouped_gemm_tm_kernel(const __grid_constant__ CUtensorMap map_w,
             // partial sums in slice order and applies SwiGLU
             if (meets && part) {
                 const int row_hi = min(t.row0 + kTmRows, t.row_end);
-                constexpr int kWide = GATE_UP ? kTmN / 2 : kTmN;
+                constexpr int kWide = GATE_UP ? WN / 2 : WN;
                 const int width = I8 ? min(kWide, p.out_cols - t.i * kWide) : kWide;
                 if (I8) {
                     if (split_tile_done<kTmEpiThreads>(p, un.tile, un.nsl, 64))
@@ -1356,7 +1362,7 @@ grouped_gemm_tm_kernel(const __grid_constant__ CUtensorMap map_w,
                 } else if (!split_tile_all_posted<kTmEpiThreads>(p, un.tile, un.nsl, 64)) {
                     if (threadIdx.x == 64) set_status(p.status, MOE_ERR_TIMEOUT);
                 } else {
-                    split_fixup_tile<kTmEpiThreads>(p, t.row0, row_hi, t.i * (kTmN / 2), kTmN / 2,
+                    split_fixup_tile<kTmEpiThreads>(p, t.row0, row_hi, t.i * (WN / 2), WN / 2,
                                                     un.nsl, un.slice, threadIdx.x - 64);
                 }
             }
@@ -1552,7 +1558,7 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w,
             float rs = 1.f;
             if (I8) {
                 rs = row < t.row_end ? i8_row_scale<GATE_UP>(p, row) : 0.f;
-                stage_scales<GATE_UP>(p, scales, t.g * p.w_group_rows + t.i * (GATE_UP ? kBM : kTmN),
+                stage_scales<GATE_UP, kTmN>(p, scales, t.g * p.w_group_rows + t.i * (GATE_UP ? kBM : kTmN),
                                       t.i * kTmN, half, lane);
             }
             const bool ready = mbar_wait(&tfull[abuf], aphase, kWaitBudgetNs, abort_flag);

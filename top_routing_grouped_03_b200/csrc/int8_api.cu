@@ -46,9 +46,11 @@ RouteLogitsLaunch rule_launch(const moe_route_rule* r) {
 
 // The K steps of a tile may be cut into slices when the tiles cannot fill the GPU; the slices'
 // int32 planes of [T, N] meet in the workspace if they take at most 64 MiB.
-constexpr int kDenseTileN = 256;
-long long dense_tiles(long long T, long long N) { return ((T + 127) / 128) * ((N + kDenseTileN - 1) / kDenseTileN); }
-bool dense_split_ok(long long T, long long N) { return 4ll * kSplitMax * T * N <= (64ll << 20) && dense_tiles(T, N) < 296; }
+constexpr int kDenseTileN = 64;  // the narrowest tile: the most tickets
+long long dense_tiles(long long T, long long N) {
+    return ((T + 127) / 128) * ((N + kDenseTileN - 1) / kDenseTileN);
+}
+bool dense_split_ok(long long T, long long N) { return 4ll * kSplitMax * T * N <= (64ll << 20) && dense_tiles(T, N) < 4 * 296; }
 
 struct DenseLayout {
     size_t status, tickets, part, xq, xs, total;

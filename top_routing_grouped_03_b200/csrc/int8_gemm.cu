@@ -32,20 +32,47 @@ __global__ void __launch_bounds__(256) gather_rows_i8_kernel(const uint4* x, con
     }
 }
 
+// CTA pairs for groups of 128 rows and more, if one group's pair tiles fill at least half of
+// the pairs (333 x 2048 x 4096 has 16 of them: 20 us in pairs).
 bool use_pairs(const Int8GemmLaunch& a, int num_sms) {
+    if (a.E == 1) {
+        const int cols = a.kind == Int8GemmLaunch::kGateUp ? 2 * a.f : a.D;
+        if (4ll * ceil_div(a.rows, CfgPair::kPairRows) * ceil_div(cols, kTmN) < num_sms) return false;
+    }
     const bool gathered = a.kind == Int8GemmLaunch::kGateUp && a.sorted_token != nullptr;
     return num_sms >= 2 && a.rows / a.E >= 128 && (!gathered || a.gather_buf != nullptr);
 }
 
+// Weight rows of a one-CTA tile.  Tiles of 256 rows reuse a token row most; when one group's
+// tiles cannot fill half of the GPU, narrower ones spread the weights over more SMs, which
+// costs less than cutting K into slices whose sums meet in memory (77 x 4104 x 2064: 30 us with
+// 256 rows and 4 slices).
+int tile_width(const Int8GemmLaunch& a, int num_sms) {
+    if (a.E != 1 || a.kind == Int8GemmLaunch::kDown) return kTmN;
+    const long long blocks = ceil_div(a.rows, kTmRows);
+    const int cols = a.kind == Int8GemmLaunch::kGateUp ? 2 * a.f : a.D;
+    for (int wn = kTmN; wn > 64; wn /= 2)
+        if (2 * blocks * ceil_div(cols, wn) > num_sms) return wn;
+    return 64;
+}
+
 template <bool GATE_UP>
-cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const Params& p, bool pair,
+cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const Params& p, bool pair, int wn,
                        int ctas, cudaStream_t s, bool pdl) {
-    const size_t ring = pair ? static_cast<size_t>(CfgPair::kStages) * CfgPair::kStageBytes
-                             : static_cast<size_t>(CfgTm::kStages) * CfgTm::kStageBytes;
-    const int stages = pair ? CfgPair::kStages : CfgTm::kStages;
+    const size_t ring = pair        ? static_cast<size_t>(CfgPair::kStages) * CfgPair::kStageBytes
+                        : wn == 256 ? static_cast<size_t>(CfgTm<256>::kStages) * CfgTm<256>::kStageBytes
+                        : wn == 128 ? static_cast<size_t>(CfgTm<128>::kStages) * CfgTm<128>::kStageBytes
+                                    : static_cast<size_t>(CfgTm<64>::kStages) * CfgTm<64>::kStageBytes;
+    const int stages = pair        ? CfgPair::kStages
+                       : wn == 256 ? CfgTm<256>::kStages
+                       : wn == 128 ? CfgTm<128>::kStages
+                                   : CfgTm<64>::kStages;
     const size_t smem = 1024 + ring + (2 * stages + 5) * 8 + 16 + 2 * (p.G + 1) * sizeof(int) +
                         (GATE_UP ? 16 : kEpiStageBytes) + kScaleBytes;
-    auto kfn = pair ? grouped_gemm_pair_kernel<GATE_UP, true> : grouped_gemm_tm_kernel<GATE_UP, true>;
+    auto kfn = pair        ? grouped_gemm_pair_kernel<GATE_UP, true>
+               : wn == 256 ? grouped_gemm_tm_kernel<GATE_UP, true, 256>
+               : wn == 128 ? grouped_gemm_tm_kernel<GATE_UP, true, 128>
+                           : grouped_gemm_tm_kernel<GATE_UP, true, 64>;
     cudaError_t err = set_smem_limit(reinterpret_cast<const void*>(kfn), smem);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg{};
@@ -101,7 +128,8 @@ cudaError_t launch_int8_gemm(const Int8GemmLaunch& a, int num_sms, cudaStream_t 
         pdl = true;
     }
     CUtensorMap mw, ma;
-    if ((err = encode_tile_map(&mw, a.w, static_cast<uint64_t>(w_group_rows) * a.E, K / 2, kBM)) !=
+    const int wn = pair ? kTmN : tile_width(a, num_sms);
+    if ((err = encode_tile_map(&mw, a.w, static_cast<uint64_t>(w_group_rows) * a.E, K / 2, wn / 2)) !=
         cudaSuccess)
         return err;
     // with a gather the activation map is not read: it covers the first row
@@ -113,7 +141,7 @@ cudaError_t launch_int8_gemm(const Int8GemmLaunch& a, int num_sms, cudaStream_t 
     p.sorted_token = a.sorted_token;
     p.sorted_w = a.sorted_w;
     p.G = a.E;
-    p.nf = gate_up ? a.f / kBM : ceil_div(a.D, kTmN);
+    p.nf = gate_up ? a.f / (wn / 2) : ceil_div(a.D, wn);
     p.nk = ceil_div(K, 2 * kBK);
     p.w_group_rows = w_group_rows;
     p.up_rows = a.f;
@@ -137,7 +165,10 @@ cudaError_t launch_int8_gemm(const Int8GemmLaunch& a, int num_sms, cudaStream_t 
                        (a.kind == Int8GemmLaunch::kDown
                             ? (a.acc_out != nullptr && a.y_out == nullptr && a.y16_out == nullptr)
                             : (a.part != nullptr && a.tickets != nullptr && a.ticket_cap > 0));
-    p.ksplit_max = split ? std::min(a.ksplit_max, kSplitSlicesMax) : 1;
+    // A dense product's slices cost a round trip of partial sums; they pay where few tiles have a
+    // long K (100 x 512 x 8192: 21 against 26 us; 77 x 4104 x 2064 the other way: 15 against 11).
+    const bool worth = !dense || (4ll * ceil_div(a.rows, kTmRows) * p.nf <= num_sms && p.nk >= 32);
+    p.ksplit_max = split && worth ? std::min(a.ksplit_max, kSplitSlicesMax) : 1;
     p.part = reinterpret_cast<float*>(a.part);
     p.part_rows = a.rows;
     p.tickets = a.tickets;
@@ -148,8 +179,8 @@ cudaError_t launch_int8_gemm(const Int8GemmLaunch& a, int num_sms, cudaStream_t 
                                  std::min(p.G, a.rows)) * p.nf * p.ksplit_max;
     const int ctas = pair ? 2 * static_cast<int>(std::min<long long>(max_tiles, num_sms / 2))
                           : static_cast<int>(std::min<long long>(max_tiles, num_sms));
-    return gate_up ? launch_one<true>(mw, ma, p, pair, ctas, s, pdl)
-                   : launch_one<false>(mw, ma, p, pair, ctas, s, pdl);
+    return gate_up ? launch_one<true>(mw, ma, p, pair, wn, ctas, s, pdl)
+                   : launch_one<false>(mw, ma, p, pair, wn, ctas, s, pdl);
 }
 
 }  // namespace moe
