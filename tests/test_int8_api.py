@@ -103,7 +103,7 @@ def test_experts_int8_refused(lib):
         return lib.moe_experts_int8(p, out, ws, size, None)
 
     assert lib.moe_experts_int8(None, ptr(), ptr(), n, None) == ARG
-    for name in ("xq", "x_scale", "expert_offsets", "sorted_token", "sorted_w", "w_gate_up",
+    for name in ("xq", "x_scale", "expert_offsets", "sorted_token", "sorted_w", "slot_to_row", "w_gate_up",
                  "gate_up_scale", "w_down", "down_scale"):
         assert call(**{name: None}) == ARG, name
     for name in ("xq", "w_gate_up", "gate_up_scale", "w_down", "down_scale", "residual"):

@@ -25,6 +25,12 @@ __device__ __forceinline__ void add8(float (&acc)[8], const uint4 v, float w) {
     acc[7] = fmaf(w, bf16_hi(v.w), acc[7]);
 }
 
+// two 16-bit integers times s
+__device__ __forceinline__ void add_pair(float& lo, float& hi, uint32_t q, float s) {
+    lo = fmaf(s, static_cast<float>(static_cast<int16_t>(q & 0xffffu)), lo);
+    hi = fmaf(s, static_cast<float>(static_cast<int32_t>(q) >> 16), hi);
+}
+
 __global__ void __launch_bounds__(256) combine_kernel(CombineLaunch a) {
     grid_dep_wait();  // the rows to combine come from the grouped GEMM
     grid_dep_launch();
@@ -68,6 +74,19 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineLaunch a) {
                 const int row = __ldg(a.slot_to_row + t * a.K + k);
                 if (row < 0) continue;  // dropped past its expert's capacity
                 add8(acc, __ldcs(ys + static_cast<size_t>(row) * vec + c), 1.f);
+            }
+        }
+        if (a.y16q_sorted) {
+            const uint4* ys = reinterpret_cast<const uint4*>(a.y16q_sorted);
+            for (int k = 0; k < a.K; ++k) {
+                const int row = __ldg(a.slot_to_row + t * a.K + k);
+                if (row < 0) continue;  // dropped past its expert's capacity
+                const uint4 q = __ldcs(ys + static_cast<size_t>(row) * vec + c);
+                const float s = __ldg(a.y16q_scale + static_cast<size_t>(row) * (a.D / 64) + c / 8);
+                add_pair(acc[0], acc[1], q.x, s);
+                add_pair(acc[2], acc[3], q.y, s);
+                add_pair(acc[4], acc[5], q.z, s);
+                add_pair(acc[6], acc[7], q.w, s);
             }
         }
         if (a.shared_out) {

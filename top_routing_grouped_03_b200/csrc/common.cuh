@@ -253,7 +253,9 @@ struct Int8GemmLaunch {
     float* h_out;    // gate_up: fp32 rows of h
     float* acc_out;  // down: [T, D] scatter-add target, or NULL
     float* y_out;    // down: [rows, D], or NULL
-    bf16* y16_out;   // down: [rows, D], or NULL; dense: [rows, N]
+    bf16* y16_out;   // dense: [rows, N]
+    int16_t* y16q_out;  // down, where int8_gemm_uses_pairs: rows [rows, D] as 16-bit integers
+    float* y16q_scale;  //   with a scale for each 64 columns [rows, D / 64], or NULL
     int* status;
     int8_t* gather_buf;  // gate_up: room for the rows in expert order [rows, D], or NULL
     float* zero_acc;     // gate_up: cleared in the kernel (zero_floats a multiple of 4)
@@ -263,6 +265,7 @@ struct Int8GemmLaunch {
     unsigned* tickets;
     int ticket_cap;
 };
+bool int8_gemm_uses_pairs(const Int8GemmLaunch& a, int num_sms);
 cudaError_t launch_int8_gemm(const Int8GemmLaunch& a, int num_sms, cudaStream_t s, bool pdl);
 
 // The same for a handful of tokens, on the CUDA cores (int8_few.cu).  x != NULL: the tokens are
@@ -302,6 +305,8 @@ struct CombineLaunch {
     const bf16* residual;  // [T, D] added before the bf16 rounding, or NULL
     const float* out_acc;
     const float* y_sorted;
+    const int16_t* y16q_sorted;  // [T*K, D] already weighted rows as 16-bit integers with a scale for
+    const float* y16q_scale;     // each 64 columns [T*K, D / 64] (instead of y_sorted), or NULL
     const bf16* y16_sorted;  // [T*K, D] bf16 rows already weighted (instead of y_sorted), or NULL
     const int32_t* slot_to_row;
     const float* topk_w;

@@ -96,6 +96,10 @@ struct Params {
     const float* col_scale;
     float* h32_out;
     int dense;
+    // down on CTA pairs: weighted rows as 16-bit integers [row][out_cols] with one scale for each
+    // 64 columns [row][out_cols / 64], or NULL
+    int16_t* y16q_out;
+    float* y16q_scale;
 };
 
 // Epilogue threads of every CTA clear their grid-strided share of p.zero_acc.
@@ -824,11 +828,34 @@ __device__ __forceinline__ void stage_scales(const Params& p, float* dst, int wr
     __syncwarp();
 }
 
-// gate_up: h (fp32) of the warp's 32 rows x hc features from feature feat on; rs: the row's scale.
+// 64 bytes of each of the warp's first n rows to dst (the first row's; rows `stride` bytes
+// apart), from v[4], this lane's row.  Stored from the lanes directly, a row's 16 bytes would be
+// half a sector (65536 x 4096 16-bit values: 454 us); transposed through `stage` (2 KB, swizzled
+// as in reduce16_transposed) an instruction covers 8 rows x 64 bytes.  cols: 16-byte chunks
+// that exist (4, or fewer at the edge of a dense product).
+__device__ __forceinline__ void store_rows64(const uint4 (&v)[4], void* dst, size_t stride, int n,
+                                             float* stage, int lane, int chunks = 4) {
+    uint4* st = reinterpret_cast<uint4*>(stage);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) st[lane * 4 + (k ^ ((lane >> 1) & 3))] = v[k];
+    __syncwarp();
+    const int r0 = lane >> 2, kq = lane & 3;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+        const int r = it * 8 + r0;
+        const uint4 o = st[r * 4 + (kq ^ ((r >> 1) & 3))];
+        if (r < n && kq < chunks)
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(dst) + r * stride + kq * 16) = o;
+    }
+    __syncwarp();
+}
+
+// gate_up: h (fp32) of the warp's first n rows, from row0 on, x hc features from feature feat on;
+// rs: the scale of this lane's row.
 __device__ __forceinline__ void i8_gate_up_epilogue(const Params& p, uint32_t tgate, uint32_t tup,
-                                                    int row, bool valid, float rs, int feat, int hc,
-                                                    const float* scales) {
-    float* hrow = p.h32_out + static_cast<size_t>(row) * p.out_cols + feat;
+                                                    int row0, int n, float rs, int feat, int hc,
+                                                    const float* scales, float* stage, int lane) {
+    float* h0 = p.h32_out + static_cast<size_t>(row0) * p.out_cols + feat;
 #pragma unroll 1
     for (int c0 = 0; c0 < hc; c0 += 16) {
         uint32_t gv[16], uv[16];
@@ -837,16 +864,13 @@ __device__ __forceinline__ void i8_gate_up_epilogue(const Params& p, uint32_t tg
         tmem_ld_wait();
         scale_columns<16>(gv, scales + c0);
         scale_columns<16>(uv, scales + hc + c0);
-        if (valid) {
-            float4* dst = reinterpret_cast<float4*>(hrow + c0);
+        uint4 v[4];
+        auto h = [&](int j) {
+            return __float_as_uint(swiglu_scaled(__uint_as_float(gv[j]), __uint_as_float(uv[j]), rs));
+        };
 #pragma unroll
-            for (int j = 0; j < 16; j += 4)
-                __stcg(dst + j / 4, make_float4(
-                    swiglu_scaled(__uint_as_float(gv[j]), __uint_as_float(uv[j]), rs),
-                    swiglu_scaled(__uint_as_float(gv[j + 1]), __uint_as_float(uv[j + 1]), rs),
-                    swiglu_scaled(__uint_as_float(gv[j + 2]), __uint_as_float(uv[j + 2]), rs),
-                    swiglu_scaled(__uint_as_float(gv[j + 3]), __uint_as_float(uv[j + 3]), rs)));
-        }
+        for (int k = 0; k < 4; ++k) v[k] = make_uint4(h(4 * k), h(4 * k + 1), h(4 * k + 2), h(4 * k + 3));
+        store_rows64(v, h0 + c0, sizeof(float) * p.out_cols, n, stage, lane);
     }
 }
 
@@ -868,24 +892,75 @@ __device__ __forceinline__ void i8_store_partials(uint32_t tcol, float* prow, in
 }
 
 // Dense product: bf16 rows of cols columns (a multiple of 8).
-__device__ __forceinline__ void i8_dense_epilogue(const Params& p, uint32_t tcol, int row, bool valid,
-                                                  float rs, int col0, int cols, const float* scales) {
-    bf16* orow = p.y16_out + static_cast<size_t>(row) * p.out_cols + col0;
+__device__ __forceinline__ void i8_dense_epilogue(const Params& p, uint32_t tcol, int row0, int n,
+                                                  float rs, int col0, int cols, const float* scales,
+                                                  float* stage, int lane) {
+    bf16* o0 = p.y16_out + static_cast<size_t>(row0) * p.out_cols + col0;
 #pragma unroll 1
-    for (int c0 = 0; c0 < cols; c0 += 16) {
-        uint32_t v[16];
-        tmem_ld16(tcol + c0, v);
+    for (int c0 = 0; c0 < cols; c0 += 32) {
+        uint32_t t[32];
+        tmem_ld32(tcol + c0, t);
         tmem_ld_wait();
+        scale_columns<32>(t, scales + c0);  // (past cols: whatever the warp's copy holds)
+        uint4 v[4];
+        auto two = [&](int j) {
+            return pack_bf16x2(rs * __uint_as_float(t[j]), rs * __uint_as_float(t[j + 1]));
+        };
 #pragma unroll
-        for (int h = 0; h < 16; h += 8) {
-            if (c0 + h >= cols) break;
-            scale_columns<8>(v + h, scales + c0 + h);
-            if (valid)
-                *reinterpret_cast<uint4*>(orow + c0 + h) = make_uint4(
-                    pack_bf16x2(rs * __uint_as_float(v[h]), rs * __uint_as_float(v[h + 1])),
-                    pack_bf16x2(rs * __uint_as_float(v[h + 2]), rs * __uint_as_float(v[h + 3])),
-                    pack_bf16x2(rs * __uint_as_float(v[h + 4]), rs * __uint_as_float(v[h + 5])),
-                    pack_bf16x2(rs * __uint_as_float(v[h + 6]), rs * __uint_as_float(v[h + 7])));
+        for (int k = 0; k < 4; ++k)
+            v[k] = make_uint4(two(8 * k), two(8 * k + 2), two(8 * k + 4), two(8 * k + 6));
+        store_rows64(v, o0 + c0, sizeof(bf16) * p.out_cols, n, stage, lane, (cols - c0) / 8);
+    }
+}
+
+// down rows for a sum over a token's experts by a later kernel: blocks of 64 columns of
+// v = w * product as 16-bit integers with the scale max |v| / 32767.  As many bytes as bf16 rows,
+// but an error of 2^-16 of the block's largest value instead of 2^-9 of each: bf16 rows would
+// add as much again to the error of the bf16 result.  fp32 reductions into the tokens' rows (1 GB
+// of them at 65536 x 4096) kept the tensor cores waiting: 454 us.
+constexpr int kRows16Block = 64;
+__device__ __forceinline__ void i8_rows16_epilogue(const Params& p, uint32_t tcol, int row0, int n,
+                                                   float w, int col0, const float* scales, float* stage,
+                                                   int lane) {
+    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to the low bits
+    int16_t* y0 = p.y16q_out + static_cast<size_t>(row0) * p.out_cols + col0;
+    float* s0 = p.y16q_scale + static_cast<size_t>(row0 + lane) * (p.out_cols / kRows16Block) +
+                col0 / kRows16Block;
+#pragma unroll 1
+    for (int b0 = 0; b0 < 128; b0 += kRows16Block) {
+        uint32_t v[kRows16Block];
+        uint32_t m = 0;
+#pragma unroll
+        for (int c0 = 0; c0 < kRows16Block; c0 += 32) {
+            uint32_t t[32];
+            tmem_ld32(tcol + b0 + c0, t);
+            tmem_ld_wait();
+            scale_columns<32>(t, scales + b0 + c0);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                v[c0 + j] = __float_as_uint(w * __uint_as_float(t[j]));
+                // on the bit patterns: a NaN (a row that has one) counts above infinity
+                m = max(m, v[c0 + j] & 0x7fffffffu);
+            }
+        }
+        const float top = __uint_as_float(m);
+        const bool fine = m < 0x7f800000u;
+        const float inv = fine && top > 1e-30f ? __fdividef(32767.f, top) : 0.f;
+        if (lane < n)
+            s0[b0 / kRows16Block] = !fine ? __int_as_float(0x7fc00000)
+                                          : top > 1e-30f ? top * (1.f / 32767.f) : 0.f;
+        auto two = [&](int j) {
+            return __byte_perm(__float_as_uint(fmaf(__uint_as_float(v[j]), inv, kMagic)),
+                               __float_as_uint(fmaf(__uint_as_float(v[j + 1]), inv, kMagic)), 0x5410);
+        };
+#pragma unroll
+        for (int c0 = 0; c0 < kRows16Block; c0 += 32) {
+            uint4 o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                o[k] = make_uint4(two(c0 + 8 * k), two(c0 + 8 * k + 2), two(c0 + 8 * k + 4),
+                                  two(c0 + 8 * k + 6));
+            store_rows64(o, y0 + b0 + c0, sizeof(int16_t) * p.out_cols, n, stage, lane);
         }
     }
 }
@@ -954,7 +1029,8 @@ __device__ __forceinline__ void tm_epilogue(const Params& p, uint32_t tbase, int
                                             const float* scales = nullptr) {
     const int lane = threadIdx.x & 31;
     // few rows in the tile: a warp without any has nothing to drain
-    if (I8 && __ballot_sync(0xffffffffu, valid) == 0) return;
+    const int n_rows = I8 ? __popc(__ballot_sync(0xffffffffu, valid)) : 0;  // the warp's first rows
+    if (I8 && n_rows == 0) return;
     if (I8 && GATE_UP) {
         const int F = wn >> 1, hc = F >> 1, feat = tile_i * F + half * hc;
         if (part) {
@@ -962,8 +1038,8 @@ __device__ __forceinline__ void tm_epilogue(const Params& p, uint32_t tbase, int
             i8_store_partials(tbase + half * hc, prow, hc, valid);
             i8_store_partials(tbase + F + half * hc, prow + p.out_cols, hc, valid);
         } else {
-            i8_gate_up_epilogue(p, tbase + half * hc, tbase + F + half * hc, row, valid, rs, feat,
-                                hc, scales);
+            i8_gate_up_epilogue(p, tbase + half * hc, tbase + F + half * hc, row - lane, n_rows, rs,
+                                feat, hc, scales, stage, lane);
         }
     } else if (I8 && p.dense) {
         // dense product; the last tile may hold fewer than wn columns
@@ -974,7 +1050,8 @@ __device__ __forceinline__ void tm_epilogue(const Params& p, uint32_t tbase, int
             i8_store_partials(tbase + half * hc, part + static_cast<size_t>(row) * p.out_cols + col0,
                               cols, valid);
         else
-            i8_dense_epilogue(p, tbase + half * hc, row, valid, rs, col0, cols, scales);
+            i8_dense_epilogue(p, tbase + half * hc, row - lane, n_rows, rs, col0, cols, scales, stage,
+                              lane);
     } else if (GATE_UP && part) {
         // one K slice of the tile: fp32 partial sums of the gate and up features
         const int F = wn >> 1;
@@ -1026,6 +1103,11 @@ __device__ __forceinline__ void tm_epilogue(const Params& p, uint32_t tbase, int
         // the last tile of an int8 launch may hold half the columns (out_cols is a multiple
         // of 128, the tile of 256)
         if (I8 && tile_i * wn + half * hc >= p.out_cols) return;
+        if (I8 && ROWS16 && p.y16q_out) {
+            i8_rows16_epilogue(p, tbase + half * hc, row - lane, n_rows, rs, tile_i * wn + half * hc,
+                               scales, stage, lane);
+            return;
+        }
         const float w = I8 ? rs : (valid && p.sorted_w) ? __ldg(p.sorted_w + row) : 1.f;
         const float* cs = scales;
         const int tok = valid ? (p.sorted_token ? __ldg(p.sorted_token + row) : row) : 0;
@@ -1113,13 +1195,11 @@ __device__ __forceinline__ float* epi_stage(int* table_end, int warp) {
     return reinterpret_cast<float*>(a) + (warp - 2) * kStageFloatsPerWarp;
 }
 
-// int8 kernels: the warps' column scales, after that staging (down) or the group table (gate_up)
+// int8 kernels: the warps' column scales, after that staging
 constexpr size_t kScaleBytes = (kTmEpiThreads / 32) * kScaleFloats * sizeof(float);
-template <bool GATE_UP>
 __device__ __forceinline__ float* scale_stage(int* table_end, int warp) {
-    float* base = epi_stage(table_end, 2);
-    if (!GATE_UP) base += (kTmEpiThreads / 32) * kStageFloatsPerWarp;
-    return base + (warp - 2) * kScaleFloats;
+    return epi_stage(table_end, 2) + (kTmEpiThreads / 32) * kStageFloatsPerWarp +
+           (warp - 2) * kScaleFloats;
 }
 
 // The scale that a row's products get: gate_up and dense the token's, down the row's own times
@@ -1312,7 +1392,7 @@ grouped_gemm_tm_kernel(const __grid_constant__ CUtensorMap map_w,
         // ---------------------------------------------------------------- epilogue
         const int q = warp & 3;
         if (GATE_UP) clear_accumulator(p, threadIdx.x - 64, kTmEpiThreads);
-        float* scales = I8 ? scale_stage<GATE_UP>(g_tile + p.G + 1, warp) : nullptr;
+        float* scales = I8 ? scale_stage(g_tile + p.G + 1, warp) : nullptr;
         uint32_t abuf = 0, aphase = 0;
         for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
             const Unit un = unit_at(units, tile);
@@ -1344,7 +1424,7 @@ grouped_gemm_tm_kernel(const __grid_constant__ CUtensorMap map_w,
                               : nullptr;
             tm_epilogue<GATE_UP, false, I8>(
                 p, tbase, row, valid, t.i, half,
-                GATE_UP ? nullptr : epi_stage(g_tile + p.G + 1, warp), WN, part, rs, scales);
+                GATE_UP && !I8 ? nullptr : epi_stage(g_tile + p.G + 1, warp), WN, part, rs, scales);
             tc_fence_before();
             mbar_arrive(&tempty[abuf]);
             abuf ^= 1u;
@@ -1549,7 +1629,7 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w,
         const int q = warp & 3;
         if (GATE_UP) clear_accumulator(p, threadIdx.x - 64, kTmEpiThreads);
         const uint32_t leader_tempty0 = map_to_rank(smem_u32(&tempty[0]), 0);
-        float* scales = I8 ? scale_stage<GATE_UP>(g_tile + p.G + 1, warp) : nullptr;
+        float* scales = I8 ? scale_stage(g_tile + p.G + 1, warp) : nullptr;
         uint32_t abuf = 0, aphase = 0;
         for (int tile = pair; tile < total; tile += npairs) {
             const Tile t = decode_tile(tile, g_tile, g_off, p.G, C::kPairRows);
@@ -1572,7 +1652,7 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w,
                                    abuf * C::kAccCols;
             tm_epilogue<GATE_UP, true, I8>(
                 p, tbase, row, row < t.row_end, t.i, half,
-                GATE_UP ? nullptr : epi_stage(g_tile + p.G + 1, warp), kTmN, nullptr, rs, scales);
+                GATE_UP && !I8 ? nullptr : epi_stage(g_tile + p.G + 1, warp), kTmN, nullptr, rs, scales);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(leader_tempty0 + abuf * 8);

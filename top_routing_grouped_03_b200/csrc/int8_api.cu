@@ -104,7 +104,7 @@ cudaError_t launch_dense(const int8_t* xq, const float* xs, const int8_t* wq, co
 // ---------------------------------------------------------------- experts
 
 struct ExpertsLayout {
-    size_t status, tickets, gather, h, hq, hs, acc, y, part, total;
+    size_t status, tickets, gather, h, hq, hs, acc, y, y_scale, part, total;
     size_t zero_end;
 };
 void take_experts(Taker& take, ExpertsLayout& L, long long T, long long D, long long E, long long K,
@@ -116,7 +116,9 @@ void take_experts(Taker& take, ExpertsLayout& L, long long T, long long D, long 
     L.hq = take(rows * f);
     L.hs = take(sizeof(float) * rows);
     L.acc = take(sizeof(float) * T * D);
-    L.y = take(det ? sizeof(float) * rows * D : 0);
+    // rows for a sum by the combine: fp32 (fixed order), 16-bit integers and scales (CTA pairs)
+    L.y = take(det ? sizeof(float) * rows * D : pairs ? sizeof(int16_t) * rows * D : 0);
+    L.y_scale = take(!det && pairs ? sizeof(float) * rows * (D / 64) : 0);
     L.part = take(gate_up_split_ok(T, K, f) ? sizeof(float) * kSplitMax * rows * 2 * f : 0);
 }
 ExpertsLayout experts_layout(long long T, long long D, long long E, long long K, long long f,
@@ -131,10 +133,14 @@ ExpertsLayout experts_layout(long long T, long long D, long long E, long long K,
     return L;
 }
 
-// gate_up, the quantised h and down of the routed experts.  acc != NULL: the weighted rows are
-// added there (zeroed here when clear_acc); otherwise y gets the unweighted rows.
-cudaError_t run_experts(const moe_int8_experts& p, const ExpertsLayout& L, void* ws, float* acc,
-                        bool clear_acc, float* y, int sms, cudaStream_t s, bool pdl) {
+// How the rows of a token's experts are summed: in the fp32 accumulator by reductions, or from
+// their rows in memory by the combine (unweighted fp32 rows in slot order; on CTA pairs, where
+// reductions would hold up the tensor cores, weighted 16-bit rows).
+enum class Sum { kAccumulator, kRows, kRows16 };
+
+// gate_up, the quantised h and down of the routed experts.  acc (or NULL) is zeroed on the way.
+cudaError_t run_experts(const moe_int8_experts& p, const ExpertsLayout& L, void* ws, Sum sum, float* acc,
+                        int sms, cudaStream_t s, bool pdl) {
     const int rows = p.T * p.K;
     Int8GemmLaunch up{};
     up.kind = Int8GemmLaunch::kGateUp;
@@ -148,7 +154,7 @@ cudaError_t run_experts(const moe_int8_experts& p, const ExpertsLayout& L, void*
     up.h_out = at<float>(ws, L.h);
     up.status = at<int>(ws, L.status);
     up.gather_buf = rows / p.E >= 128 ? at<int8_t>(ws, L.gather) : nullptr;
-    if (clear_acc) {
+    if (acc) {
         up.zero_acc = acc;
         up.zero_floats = static_cast<long long>(p.T) * p.D;
     }
@@ -177,13 +183,46 @@ cudaError_t run_experts(const moe_int8_experts& p, const ExpertsLayout& L, void*
     dn.act_scale = q.scale;
     dn.offsets = p.expert_offsets;
     dn.sorted_token = p.sorted_token;
-    dn.sorted_w = acc ? p.sorted_w : nullptr;
+    dn.sorted_w = sum == Sum::kRows ? nullptr : p.sorted_w;
     dn.rows = rows; dn.tokens = p.T; dn.E = p.E; dn.D = p.D; dn.f = p.f;
-    dn.acc_out = acc;
-    dn.y_out = y;
+    if (sum == Sum::kAccumulator) dn.acc_out = acc;
+    if (sum == Sum::kRows) dn.y_out = at<float>(ws, L.y);
+    if (sum == Sum::kRows16) {
+        dn.y16q_out = at<int16_t>(ws, L.y);
+        dn.y16q_scale = at<float>(ws, L.y_scale);
+    }
     dn.status = up.status;
-    dn.ksplit_max = acc ? kSplitMax : 1;
+    dn.ksplit_max = sum == Sum::kAccumulator ? kSplitMax : 1;
     return launch_int8_gemm(dn, sms, s, true);
+}
+
+Sum pick_sum(int T, int D, int E, int K, int f, unsigned flags, int sms) {
+    if (flags & MOE_FLAG_DETERMINISTIC) return Sum::kRows;
+    Int8GemmLaunch dn{};
+    dn.kind = Int8GemmLaunch::kDown;
+    dn.rows = T * K; dn.tokens = T; dn.E = E; dn.D = D; dn.f = f;
+    return T * K / E >= 128 && int8_gemm_uses_pairs(dn, sms) ? Sum::kRows16 : Sum::kAccumulator;
+}
+
+// The end of a call: the accumulator (or NULL), the rows and the residual to out.
+cudaError_t run_combine(const ExpertsLayout& L, void* ws, Sum sum, const float* acc,
+                        const int32_t* slot_to_row, const float* topk_w, const moe_bf16* residual, int T,
+                        int D, int K, moe_bf16* out, int sms, cudaStream_t s) {
+    CombineLaunch c{};
+    c.residual = reinterpret_cast<const bf16*>(residual);
+    c.out_acc = acc;
+    c.slot_to_row = slot_to_row;
+    if (sum == Sum::kRows) {
+        c.y_sorted = at<float>(ws, L.y);
+        c.topk_w = topk_w;
+    }
+    if (sum == Sum::kRows16) {
+        c.y16q_sorted = at<int16_t>(ws, L.y);
+        c.y16q_scale = at<float>(ws, L.y_scale);
+    }
+    c.T = T; c.D = D; c.K = K;
+    c.out = reinterpret_cast<bf16*>(out);
+    return launch_combine(c, sms, s, true);
 }
 
 // The whole of moe_experts_int8 for a handful of rows: two launches.
@@ -342,13 +381,10 @@ int layer_int8(const moe_layer_params* p, const RouteLogitsLaunch* rule, const m
     e.T = T; e.D = D; e.E = E; e.K = K; e.f = f;
     if (!shared && few_experts_ok(T, D, K, f))
         return run_few(e, at<float>(ws, L.x.h), out, sms, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
-    float* acc = at<float>(ws, L.x.acc);
-    float* y = det ? at<float>(ws, L.x.y) : nullptr;
-    if (det && shared &&
-        cudaMemsetAsync(acc, 0, sizeof(float) * static_cast<size_t>(T) * D, s) != cudaSuccess)
-        return MOE_ERR_CUDA;
-    if (run_experts(e, L.x, ws, det ? nullptr : acc, !det, y, sms, s, !(det && shared)) != cudaSuccess)
-        return MOE_ERR_CUDA;
+    const Sum sum = pick_sum(T, D, E, K, f, p->flags, sms);
+    // the accumulator: the routed rows' reductions and the shared expert's
+    float* acc = sum == Sum::kAccumulator || shared ? at<float>(ws, L.x.acc) : nullptr;
+    if (run_experts(e, L.x, ws, sum, acc, sms, s, true) != cudaSuccess) return MOE_ERR_CUDA;
     if (shared) {
         Int8GemmLaunch su{};
         su.kind = Int8GemmLaunch::kGateUp;
@@ -383,15 +419,10 @@ int layer_int8(const moe_layer_params* p, const RouteLogitsLaunch* rule, const m
         sd.ksplit_max = det ? 1 : kSplitMax;
         if (launch_int8_gemm(sd, sms, s, true) != cudaSuccess) return MOE_ERR_CUDA;
     }
-    CombineLaunch c{};
-    c.residual = reinterpret_cast<const bf16*>(p->residual);
-    c.out_acc = det && !shared ? nullptr : acc;
-    c.y_sorted = y;
-    c.slot_to_row = pm.slot_to_row;
-    c.topk_w = det ? r.topk_w : nullptr;
-    c.T = T; c.D = D; c.K = K;
-    c.out = reinterpret_cast<bf16*>(out);
-    return launch_combine(c, sms, s, true) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return run_combine(L.x, ws, sum, acc, pm.slot_to_row, r.topk_w, p->residual, T, D, K, out, sms, s) ==
+                   cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
 }
 
 }  // namespace
@@ -543,7 +574,7 @@ int moe_experts_int8(const moe_int8_experts* p, moe_bf16* out, void* workspace, 
     if (!p->expert_offsets || !p->w_gate_up || !p->gate_up_scale || !p->w_down || !p->down_scale)
         return MOE_ERR_ARG;
     if (T > 0 && (!p->xq || !p->x_scale || !p->sorted_token || !p->sorted_w || !out)) return MOE_ERR_ARG;
-    if (T > 0 && det && (!p->slot_to_row || !p->topk_w)) return MOE_ERR_ARG;
+    if (T > 0 && (!p->slot_to_row || (det && !p->topk_w))) return MOE_ERR_ARG;
     const void* ptrs[] = {p->xq, p->w_gate_up, p->gate_up_scale, p->w_down, p->down_scale, p->residual, out};
     for (const void* q : ptrs)
         if (!aligned16(q)) return MOE_ERR_ALIGN;
@@ -556,18 +587,13 @@ int moe_experts_int8(const moe_int8_experts* p, moe_bf16* out, void* workspace, 
     if (few_experts_ok(T, D, K, f))
         return run_few(*p, at<float>(workspace, L.h), out, sms, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     if (cudaMemsetAsync(workspace, 0, L.zero_end, s) != cudaSuccess) return MOE_ERR_CUDA;
-    float* acc = det ? nullptr : at<float>(workspace, L.acc);
-    float* y = det ? at<float>(workspace, L.y) : nullptr;
-    if (run_experts(*p, L, workspace, acc, true, y, sms, s, false) != cudaSuccess) return MOE_ERR_CUDA;
-    CombineLaunch c{};
-    c.residual = reinterpret_cast<const bf16*>(p->residual);
-    c.out_acc = acc;
-    c.y_sorted = y;
-    c.slot_to_row = p->slot_to_row;
-    c.topk_w = det ? p->topk_w : nullptr;
-    c.T = T; c.D = D; c.K = K;
-    c.out = reinterpret_cast<bf16*>(out);
-    return launch_combine(c, sms, s, true) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    const Sum sum = pick_sum(T, D, E, K, f, p->flags, sms);
+    float* acc = sum == Sum::kAccumulator ? at<float>(workspace, L.acc) : nullptr;
+    if (run_experts(*p, L, workspace, sum, acc, sms, s, false) != cudaSuccess) return MOE_ERR_CUDA;
+    return run_combine(L, workspace, sum, acc, p->slot_to_row, p->topk_w, p->residual, T, D, K, out, sms,
+                       s) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
 }
 
 size_t moe_layer_ex_workspace_size(int T, int D, int E, int K, int f, int f_s, unsigned flags, int int8) {

@@ -19,16 +19,27 @@
 namespace moe {
 namespace {
 
-// Rows in expert order for the CTA-pair kernel: out[r] = x[tok[r]] for r < *row_count.
+// Rows in expert order for the CTA-pair kernel: out[r] = x[tok[r]] for r < *row_count, a warp to
+// a row, four 16-byte loads of each lane in flight.
 __global__ void __launch_bounds__(256) gather_rows_i8_kernel(const uint4* x, const int32_t* tok,
                                                              const int32_t* row_count, int rows,
                                                              int vec, uint4* out) {
     grid_dep_wait();
     grid_dep_launch();
-    const long long n = static_cast<long long>(row_count ? min(*row_count, rows) : rows) * vec;
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += 256ll * gridDim.x) {
-        const long long r = i / vec;
-        out[i] = __ldg(x + static_cast<long long>(__ldg(tok + r)) * vec + (i - r * vec));
+    const int n = row_count ? min(*row_count, rows) : rows;
+    const int lane = threadIdx.x & 31;
+    for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < n; r += gridDim.x * 8) {
+        const uint4* src = x + static_cast<size_t>(__ldg(tok + r)) * vec;
+        uint4* dst = out + static_cast<size_t>(r) * vec;
+        for (int i0 = lane; i0 < vec; i0 += 128) {
+            uint4 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i0 + 32 * u < vec) v[u] = __ldg(src + i0 + 32 * u);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i0 + 32 * u < vec) dst[i0 + 32 * u] = v[u];
+        }
     }
 }
 
@@ -68,7 +79,7 @@ cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const Param
                        : wn == 128 ? CfgTm<128>::kStages
                                    : CfgTm<64>::kStages;
     const size_t smem = 1024 + ring + (2 * stages + 5) * 8 + 16 + 2 * (p.G + 1) * sizeof(int) +
-                        (GATE_UP ? 16 : kEpiStageBytes) + kScaleBytes;
+                        kEpiStageBytes + kScaleBytes;
     auto kfn = pair        ? grouped_gemm_pair_kernel<GATE_UP, true>
                : wn == 256 ? grouped_gemm_tm_kernel<GATE_UP, true, 256>
                : wn == 128 ? grouped_gemm_tm_kernel<GATE_UP, true, 128>
@@ -102,6 +113,8 @@ cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const Param
 }  // namespace
 
 
+bool int8_gemm_uses_pairs(const Int8GemmLaunch& a, int num_sms) { return use_pairs(a, num_sms); }
+
 cudaError_t launch_int8_gemm(const Int8GemmLaunch& a, int num_sms, cudaStream_t s, bool pdl) {
     if (a.rows == 0) return cudaSuccess;
     if (a.E > kMaxGroups) return cudaErrorInvalidValue;
@@ -115,9 +128,7 @@ cudaError_t launch_int8_gemm(const Int8GemmLaunch& a, int num_sms, cudaStream_t 
     cudaError_t err;
     if (pair && gather) {
         const int vec = K / 16;
-        const long long n = static_cast<long long>(a.rows) * vec;
-        err = launch_kernel(gather_rows_i8_kernel,
-                            dim3(static_cast<unsigned>(std::min<long long>((n + 255) / 256, 8ll * num_sms))),
+        err = launch_kernel(gather_rows_i8_kernel, dim3(std::min(ceil_div(a.rows, 8), 8 * num_sms)),
                             dim3(256), 0, s, pdl, reinterpret_cast<const uint4*>(act), a.sorted_token,
                             a.offsets ? a.offsets + a.E : nullptr, a.rows, vec,
                             reinterpret_cast<uint4*>(a.gather_buf));
@@ -149,6 +160,8 @@ cudaError_t launch_int8_gemm(const Int8GemmLaunch& a, int num_sms, cudaStream_t 
     p.acc_out = a.acc_out;
     p.y_out = a.y_out;
     p.y16_out = a.y16_out;
+    p.y16q_out = pair ? a.y16q_out : nullptr;
+    p.y16q_scale = a.y16q_scale;
     p.status = a.status;
     p.gather_tok = gather ? a.sorted_token : nullptr;
     p.x = reinterpret_cast<const bf16*>(act);
