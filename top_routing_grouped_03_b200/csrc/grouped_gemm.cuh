@@ -783,7 +783,7 @@ __device__ __forceinline__ void split_fixup_tile(const Params& p, int row0, int 
 // the weight row's fp32 scales.
 
 // v[j] (int32 bits) -> fp32 bits of v[j] * cs[j]; cs: 16-byte aligned, the same for all lanes
-// (the warp's copy of its columns' scales in shared memory, see stage_scales, or global)
+// (the warp's copy of its columns' scales in shared memory, see load_scales, or global)
 template <int N>
 __device__ __forceinline__ void scale_columns(uint32_t* v, const float* cs) {
 #pragma unroll
@@ -805,15 +805,14 @@ __device__ __forceinline__ float row_scale_of(const Params& p, int row) {
     return __ldg(p.row_scale + (p.scale_tok ? __ldg(p.scale_tok + row) : row));
 }
 
-// The column scales of a warp's share of a tile into its 128 floats of shared memory: gate_up
-// WN / 4 gate and as many up features, otherwise WN / 2 output columns.  Issued before the
-// wait for the accumulator, so that the loads (weights' scales come from HBM) overlap the
-// products.
+// The column scales of a warp's share of a tile (gate_up: WN / 4 gate and as many up features,
+// otherwise WN / 2 output columns), four to a lane: loaded one tile ahead, so that the loads
+// (weights' scales come from HBM) overlap the tile before, and put into the warp's 128 floats
+// of shared memory when their tile begins.
 constexpr int kScaleFloats = 128;
 template <bool GATE_UP, int WN>
-__device__ __forceinline__ void stage_scales(const Params& p, float* dst, int wr, int col0, int half,
-                                             int lane) {
-    constexpr int kLanes = WN / 8;  // lanes that load four scales each
+__device__ __forceinline__ float4 load_scales(const Params& p, int wr, int col0, int half, int lane) {
+    constexpr int kLanes = WN / 8;
     const float* src;
     bool in = lane < kLanes;
     if (GATE_UP) {
@@ -823,8 +822,11 @@ __device__ __forceinline__ void stage_scales(const Params& p, float* dst, int wr
         src = p.col_scale + wr + half * (WN / 2) + 4 * lane;
         in = in && col0 + half * (WN / 2) + 4 * lane < p.out_cols;
     }
+    return in ? __ldg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+__device__ __forceinline__ void put_scales(float* dst, float4 v, int lane) {
     __syncwarp();  // the last tile's reads are over
-    if (in) *reinterpret_cast<float4*>(dst + 4 * lane) = __ldg(reinterpret_cast<const float4*>(src));
+    *reinterpret_cast<float4*>(dst + 4 * lane) = v;
     __syncwarp();
 }
 
@@ -928,39 +930,33 @@ __device__ __forceinline__ void i8_rows16_epilogue(const Params& p, uint32_t tco
                 col0 / kRows16Block;
 #pragma unroll 1
     for (int b0 = 0; b0 < 128; b0 += kRows16Block) {
-        uint32_t v[kRows16Block];
-        uint32_t m = 0;
+        uint32_t v[2][32];
+        tmem_ld32(tcol + b0, v[0]);
+        tmem_ld32(tcol + b0 + 32, v[1]);
+        tmem_ld_wait();
+        // the row's factor w goes into the block's scale
+        float top = 0.f;
 #pragma unroll
-        for (int c0 = 0; c0 < kRows16Block; c0 += 32) {
-            uint32_t t[32];
-            tmem_ld32(tcol + b0 + c0, t);
-            tmem_ld_wait();
-            scale_columns<32>(t, scales + b0 + c0);
+        for (int c = 0; c < 2; ++c) {
+            scale_columns<32>(v[c], scales + b0 + 32 * c);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                v[c0 + j] = __float_as_uint(w * __uint_as_float(t[j]));
-                // on the bit patterns: a NaN (a row that has one) counts above infinity
-                m = max(m, v[c0 + j] & 0x7fffffffu);
-            }
+            for (int j = 0; j < 32; ++j) top = fmaxf(top, fabsf(__uint_as_float(v[c][j])));
         }
-        const float top = __uint_as_float(m);
-        const bool fine = m < 0x7f800000u;
-        const float inv = fine && top > 1e-30f ? __fdividef(32767.f, top) : 0.f;
-        if (lane < n)
-            s0[b0 / kRows16Block] = !fine ? __int_as_float(0x7fc00000)
-                                          : top > 1e-30f ? top * (1.f / 32767.f) : 0.f;
-        auto two = [&](int j) {
-            return __byte_perm(__float_as_uint(fmaf(__uint_as_float(v[j]), inv, kMagic)),
-                               __float_as_uint(fmaf(__uint_as_float(v[j + 1]), inv, kMagic)), 0x5410);
-        };
+        const bool any = top > 1e-30f && top < INFINITY;
+        const float inv = any ? __fdividef(32767.f, top) : 0.f;
+        // (a NaN comes in by w; products that overflow make their block NaN)
+        if (lane < n) s0[b0 / kRows16Block] = any ? w * (top * (1.f / 32767.f)) : w * (top < 1.f ? 0.f : NAN);
 #pragma unroll
-        for (int c0 = 0; c0 < kRows16Block; c0 += 32) {
+        for (int c = 0; c < 2; ++c) {
+            auto two = [&](int j) {
+                return __byte_perm(__float_as_uint(fmaf(__uint_as_float(v[c][j]), inv, kMagic)),
+                                   __float_as_uint(fmaf(__uint_as_float(v[c][j + 1]), inv, kMagic)), 0x5410);
+            };
             uint4 o[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                o[k] = make_uint4(two(c0 + 8 * k), two(c0 + 8 * k + 2), two(c0 + 8 * k + 4),
-                                  two(c0 + 8 * k + 6));
-            store_rows64(o, y0 + b0 + c0, sizeof(int16_t) * p.out_cols, n, stage, lane);
+                o[k] = make_uint4(two(8 * k), two(8 * k + 2), two(8 * k + 4), two(8 * k + 6));
+            store_rows64(o, y0 + b0 + 32 * c, sizeof(int16_t) * p.out_cols, n, stage, lane);
         }
     }
 }
@@ -1211,6 +1207,22 @@ __device__ __forceinline__ float i8_row_scale(const Params& p, int row) {
     return s;
 }
 
+// A tile's scales for one epilogue warp: its lane's row (row_in_tile) and four columns.
+struct TileScales {
+    float row;
+    float4 col;
+};
+template <bool GATE_UP, int WN>
+__device__ __forceinline__ TileScales tile_scales(const Params& p, const Tile& t, int row_in_tile, int half,
+                                                  int lane) {
+    const int row = t.row0 + row_in_tile;
+    TileScales s;
+    s.col = load_scales<GATE_UP, WN>(p, t.g * p.w_group_rows + t.i * (GATE_UP ? WN / 2 : WN), t.i * WN,
+                                     half, lane);
+    s.row = row < t.row_end ? i8_row_scale<GATE_UP>(p, row) : 0.f;
+    return s;
+}
+
 // WN: weight rows of a tile (256; the int8 kernels also 128 and 64, see int8_gemm.cu).
 template <int WN = kTmN>
 struct CfgTm {
@@ -1392,19 +1404,28 @@ grouped_gemm_tm_kernel(const __grid_constant__ CUtensorMap map_w,
         // ---------------------------------------------------------------- epilogue
         const int q = warp & 3;
         if (GATE_UP) clear_accumulator(p, threadIdx.x - 64, kTmEpiThreads);
+        const int half = (warp - 2) >> 2;
         float* scales = I8 ? scale_stage(g_tile + p.G + 1, warp) : nullptr;
         uint32_t abuf = 0, aphase = 0;
+        TileScales next{};
+        if (I8 && static_cast<int>(blockIdx.x) < total)
+            next = tile_scales<GATE_UP, WN>(
+                p, decode_tile(unit_at(units, blockIdx.x).tile, g_tile, g_off, p.G, kTmRows), q * 32 + lane,
+                half, lane);
         for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
             const Unit un = unit_at(units, tile);
             const Tile t = decode_tile(un.tile, g_tile, g_off, p.G, kTmRows);
             const int row = t.row0 + q * 32 + lane;
             const bool valid = row < t.row_end;
-            const int half = (warp - 2) >> 2;
             const int wr = t.g * p.w_group_rows + t.i * (GATE_UP ? WN / 2 : WN);
-            float rs = 1.f;
+            const float rs = next.row;
             if (I8) {
-                rs = valid ? i8_row_scale<GATE_UP>(p, row) : 0.f;
-                stage_scales<GATE_UP, WN>(p, scales, wr, t.i * WN, half, lane);
+                put_scales(scales, next.col, lane);
+                const int after = tile + static_cast<int>(gridDim.x);
+                if (after < total)
+                    next = tile_scales<GATE_UP, WN>(
+                        p, decode_tile(unit_at(units, after).tile, g_tile, g_off, p.G, kTmRows),
+                        q * 32 + lane, half, lane);
             }
             const bool ready = mbar_wait(&tfull[abuf], aphase, kWaitBudgetNs, abort_flag);
             if (!epilogue_bar_and<kTmEpiThreads>(ready)) {
@@ -1629,20 +1650,31 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w,
         const int q = warp & 3;
         if (GATE_UP) clear_accumulator(p, threadIdx.x - 64, kTmEpiThreads);
         const uint32_t leader_tempty0 = map_to_rank(smem_u32(&tempty[0]), 0);
+        const int half = (warp - 2) >> 2;
+        const int row_in_tile = static_cast<int>(rank) * kTmRows + q * 32 + lane;
         float* scales = I8 ? scale_stage(g_tile + p.G + 1, warp) : nullptr;
         uint32_t abuf = 0, aphase = 0;
+        TileScales next{};
+        if (I8 && pair < total)
+            next = tile_scales<GATE_UP, kTmN>(p, decode_tile(pair, g_tile, g_off, p.G, C::kPairRows),
+                                              row_in_tile, half, lane);
         for (int tile = pair; tile < total; tile += npairs) {
             const Tile t = decode_tile(tile, g_tile, g_off, p.G, C::kPairRows);
-            const int row = t.row0 + static_cast<int>(rank) * kTmRows + q * 32 + lane;
-            const int half = (warp - 2) >> 2;
-            float rs = 1.f;
+            const int row = t.row0 + row_in_tile;
+            const float rs = next.row;
             if (I8) {
-                rs = row < t.row_end ? i8_row_scale<GATE_UP>(p, row) : 0.f;
-                stage_scales<GATE_UP, kTmN>(p, scales, t.g * p.w_group_rows + t.i * (GATE_UP ? kBM : kTmN),
-                                      t.i * kTmN, half, lane);
+                put_scales(scales, next.col, lane);
+                if (tile + npairs < total)
+                    next = tile_scales<GATE_UP, kTmN>(
+                        p, decode_tile(tile + npairs, g_tile, g_off, p.G, C::kPairRows), row_in_tile, half,
+                        lane);
             }
-            const bool ready = mbar_wait(&tfull[abuf], aphase, kWaitBudgetNs, abort_flag);
-            if (!epilogue_bar_and<kTmEpiThreads>(ready)) {
+            bool ready = mbar_wait(&tfull[abuf], aphase, kWaitBudgetNs, abort_flag);
+            // (int8: nothing below needs the epilogue warps together; one that gives up raises the
+            // abort flag, which ends the others' next wait)
+            if (!I8) ready = epilogue_bar_and<kTmEpiThreads>(ready);
+            else ready = __all_sync(0xffffffffu, ready);
+            if (!ready) {
                 set_status(p.status, MOE_ERR_TIMEOUT);
                 *abort_flag = 1;
                 break;
