@@ -67,6 +67,8 @@ int tile_width(const Int8GemmLaunch& a, int num_sms) {
     return 64;
 }
 
+constexpr int kPairSplit = 2;
+
 template <bool GATE_UP>
 cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const Params& p, bool pair, int wn,
                        int ctas, cudaStream_t s, bool pdl) {
@@ -80,7 +82,7 @@ cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const Param
                                    : CfgTm<64>::kStages;
     const size_t smem = 1024 + ring + (2 * stages + 5) * 8 + 16 + 2 * (p.G + 1) * sizeof(int) +
                         kEpiStageBytes + kScaleBytes;
-    auto kfn = pair        ? grouped_gemm_pair_kernel<GATE_UP, true>
+    auto kfn = pair        ? grouped_gemm_pair_kernel<GATE_UP, true, kPairSplit>
                : wn == 256 ? grouped_gemm_tm_kernel<GATE_UP, true, 256>
                : wn == 128 ? grouped_gemm_tm_kernel<GATE_UP, true, 128>
                            : grouped_gemm_tm_kernel<GATE_UP, true, 64>;
@@ -88,7 +90,7 @@ cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const Param
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kTmThreads);
+    cfg.blockDim = dim3(pair ? 64 + 128 * kPairSplit : kTmThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
