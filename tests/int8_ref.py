@@ -123,10 +123,10 @@ def experts(xq, xs, idx, w, gu, gus, dn, dns, keep=None, residual=None, shared=N
         np.add.at(size, t, np.abs(v * w[t, k][:, None]))
         if T * K // gu.shape[0] >= 128:
             # many rows per expert: the weighted rows pass through 16-bit integers in blocks of
-            # 64 columns, rint(v 32767 / top) with top = max |v|: half a step is top / 65534, and
+            # 32 columns, rint(v 32767 / top) with top = max |v|: half a step is top / 65534, and
             # the factor's error of 2^-21 on numbers up to 32767 adds 1/64 of a step
-            top = np.abs(v * w[t, k][:, None]).reshape(len(t), D // 64, 64).max(2)
-            np.add.at(err, t, np.repeat(top, 64, axis=1) * (0.5 + 1 / 64) / 32767)
+            top = np.abs(v * w[t, k][:, None]).reshape(len(t), D // 32, 32).max(2)
+            np.add.at(err, t, np.repeat(top, 32, axis=1) * (0.5 + 1 / 64) / 32767)
     if shared is not None:
         gate, *weights = shared
         v, dv = _expert_rows(xq, xs, *weights)

@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineLaunch a) {
                 const int row = __ldg(a.slot_to_row + t * a.K + k);
                 if (row < 0) continue;  // dropped past its expert's capacity
                 const uint4 q = __ldcs(ys + static_cast<size_t>(row) * vec + c);
-                const float s = __ldg(a.y16q_scale + static_cast<size_t>(row) * (a.D / 64) + c / 8);
+                const float s = __ldg(a.y16q_scale + static_cast<size_t>(row) * (a.D / 32) + c / 4);
                 add_pair(acc[0], acc[1], q.x, s);
                 add_pair(acc[2], acc[3], q.y, s);
                 add_pair(acc[4], acc[5], q.z, s);

@@ -255,7 +255,7 @@ struct Int8GemmLaunch {
     float* y_out;    // down: [rows, D], or NULL
     bf16* y16_out;   // dense: [rows, N]
     int16_t* y16q_out;  // down, where int8_gemm_uses_pairs: rows [rows, D] as 16-bit integers
-    float* y16q_scale;  //   with a scale for each 64 columns [rows, D / 64], or NULL
+    float* y16q_scale;  //   with a scale for each 32 columns [rows, D / 32], or NULL
     int* status;
     int8_t* gather_buf;  // gate_up: room for the rows in expert order [rows, D], or NULL
     float* zero_acc;     // gate_up: cleared in the kernel (zero_floats a multiple of 4)
@@ -306,7 +306,7 @@ struct CombineLaunch {
     const float* out_acc;
     const float* y_sorted;
     const int16_t* y16q_sorted;  // [T*K, D] already weighted rows as 16-bit integers with a scale for
-    const float* y16q_scale;     // each 64 columns [T*K, D / 64] (instead of y_sorted), or NULL
+    const float* y16q_scale;     // each 32 columns [T*K, D / 32] (instead of y_sorted), or NULL
     const bf16* y16_sorted;  // [T*K, D] bf16 rows already weighted (instead of y_sorted), or NULL
     const int32_t* slot_to_row;
     const float* topk_w;

@@ -97,7 +97,7 @@ struct Params {
     float* h32_out;
     int dense;
     // down on CTA pairs: weighted rows as 16-bit integers [row][out_cols] with one scale for each
-    // 64 columns [row][out_cols / 64], or NULL
+    // 32 columns [row][out_cols / 32], or NULL
     int16_t* y16q_out;
     float* y16q_scale;
 };
@@ -805,22 +805,21 @@ __device__ __forceinline__ float row_scale_of(const Params& p, int row) {
     return __ldg(p.row_scale + (p.scale_tok ? __ldg(p.scale_tok + row) : row));
 }
 
-// The column scales of a warp's share of a tile (gate_up: WN / 2 / SPLIT gate and as many up
-// features, otherwise WN / SPLIT output columns), four to a lane: loaded one tile ahead, so that
-// the loads (weights' scales come from HBM) overlap the tile before, and put into the warp's
-// WN / SPLIT floats of shared memory when their tile begins.  SPLIT: warps that share a tile's
-// columns.
-template <bool GATE_UP, int WN, int SPLIT>
-__device__ __forceinline__ float4 load_scales(const Params& p, int wr, int col0, int share, int lane) {
-    constexpr int kLanes = WN / SPLIT / 4;
+// The column scales of a warp's share of a tile (gate_up: WN / 4 gate and as many up features,
+// otherwise WN / 2 output columns), four to a lane: loaded one tile ahead, so that the loads
+// (weights' scales come from HBM) overlap the tile before, and put into the warp's WN / 2 floats
+// of shared memory when their tile begins.
+template <bool GATE_UP, int WN>
+__device__ __forceinline__ float4 load_scales(const Params& p, int wr, int col0, int half, int lane) {
+    constexpr int kLanes = WN / 8;
     const float* src;
     bool in = lane < kLanes;
     if (GATE_UP) {
-        src = p.col_scale + wr + share * (WN / 2 / SPLIT) +
+        src = p.col_scale + wr + half * (WN / 4) +
               (lane < kLanes / 2 ? 4 * lane : p.up_rows + 4 * (lane - kLanes / 2));
     } else {
-        src = p.col_scale + wr + share * (WN / SPLIT) + 4 * lane;
-        in = in && col0 + share * (WN / SPLIT) + 4 * lane < p.out_cols;
+        src = p.col_scale + wr + half * (WN / 2) + 4 * lane;
+        in = in && col0 + half * (WN / 2) + 4 * lane < p.out_cols;
     }
     return in ? __ldg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
 }
@@ -831,26 +830,22 @@ __device__ __forceinline__ void put_scales(float* dst, float4 v, int lane) {
     __syncwarp();
 }
 
-// CH x 16 bytes of each of the warp's first n rows to dst (the first row's; rows `stride` bytes
+// 64 bytes of each of the warp's first n rows to dst (the first row's; rows `stride` bytes
 // apart), from v, this lane's row.  Stored from the lanes directly, a row's 16 bytes would be
-// half a sector (65536 x 4096 16-bit values: 454 us); transposed through `stage` (CH x 512 bytes,
-// swizzled against bank conflicts) an instruction covers 32 / CH rows x CH x 16 bytes.
-// chunks: 16-byte chunks that exist (CH, or fewer at the edge of a dense product).
-template <int CH>
-__device__ __forceinline__ void store_rows(const uint4 (&v)[CH], void* dst, size_t stride, int n,
-                                           float* stage, int lane, int chunks = CH) {
-    static_assert(CH == 2 || CH == 4, "");
+// half a sector (65536 x 4096 16-bit values: 454 us); transposed through `stage` (2 KB, swizzled
+// as in reduce16_transposed) an instruction covers 8 rows x 64 bytes.  chunks: 16-byte chunks
+// that exist (4, or fewer at the edge of a dense product).
+__device__ __forceinline__ void store_rows64(const uint4 (&v)[4], void* dst, size_t stride, int n,
+                                             float* stage, int lane, int chunks = 4) {
     uint4* st = reinterpret_cast<uint4*>(stage);
-    // 8 lanes' 16-byte accesses cover the 32 banks once: rows in groups of 8 / CH share a swizzle
-    auto at = [](int r, int k) { return r * CH + (k ^ ((r / (8 / CH)) & (CH - 1))); };
 #pragma unroll
-    for (int k = 0; k < CH; ++k) st[at(lane, k)] = v[k];
+    for (int k = 0; k < 4; ++k) st[lane * 4 + (k ^ ((lane >> 1) & 3))] = v[k];
     __syncwarp();
-    const int r0 = lane / CH, kq = lane % CH;
+    const int r0 = lane >> 2, kq = lane & 3;
 #pragma unroll
-    for (int it = 0; it < CH; ++it) {
-        const int r = it * (32 / CH) + r0;
-        const uint4 o = st[at(r, kq)];
+    for (int it = 0; it < 4; ++it) {
+        const int r = it * 8 + r0;
+        const uint4 o = st[r * 4 + (kq ^ ((r >> 1) & 3))];
         if (r < n && kq < chunks)
             *reinterpret_cast<uint4*>(static_cast<uint8_t*>(dst) + r * stride + kq * 16) = o;
     }
@@ -859,7 +854,6 @@ __device__ __forceinline__ void store_rows(const uint4 (&v)[CH], void* dst, size
 
 // gate_up: h (fp32) of the warp's first n rows, from row0 on, x hc features from feature feat on;
 // rs: the scale of this lane's row.
-template <int CH>
 __device__ __forceinline__ void i8_gate_up_epilogue(const Params& p, uint32_t tgate, uint32_t tup,
                                                     int row0, int n, float rs, int feat, int hc,
                                                     const float* scales, float* stage, int lane) {
@@ -872,17 +866,13 @@ __device__ __forceinline__ void i8_gate_up_epilogue(const Params& p, uint32_t tg
         tmem_ld_wait();
         scale_columns<16>(gv, scales + c0);
         scale_columns<16>(uv, scales + hc + c0);
+        uint4 v[4];
         auto h = [&](int j) {
             return __float_as_uint(swiglu_scaled(__uint_as_float(gv[j]), __uint_as_float(uv[j]), rs));
         };
 #pragma unroll
-        for (int c = 0; c < 16; c += 4 * CH) {
-            uint4 v[CH];
-#pragma unroll
-            for (int k = 0; k < CH; ++k)
-                v[k] = make_uint4(h(c + 4 * k), h(c + 4 * k + 1), h(c + 4 * k + 2), h(c + 4 * k + 3));
-            store_rows<CH>(v, h0 + c0 + c, sizeof(float) * p.out_cols, n, stage, lane);
-        }
+        for (int k = 0; k < 4; ++k) v[k] = make_uint4(h(4 * k), h(4 * k + 1), h(4 * k + 2), h(4 * k + 3));
+        store_rows64(v, h0 + c0, sizeof(float) * p.out_cols, n, stage, lane);
     }
 }
 
@@ -904,7 +894,6 @@ __device__ __forceinline__ void i8_store_partials(uint32_t tcol, float* prow, in
 }
 
 // Dense product: bf16 rows of cols columns (a multiple of 8).
-template <int CH>
 __device__ __forceinline__ void i8_dense_epilogue(const Params& p, uint32_t tcol, int row0, int n,
                                                   float rs, int col0, int cols, const float* scales,
                                                   float* stage, int lane) {
@@ -918,65 +907,57 @@ __device__ __forceinline__ void i8_dense_epilogue(const Params& p, uint32_t tcol
         auto two = [&](int j) {
             return pack_bf16x2(rs * __uint_as_float(t[j]), rs * __uint_as_float(t[j + 1]));
         };
+        uint4 v[4];
 #pragma unroll
-        for (int c = 0; c < 32; c += 8 * CH) {
-            uint4 v[CH];
-#pragma unroll
-            for (int k = 0; k < CH; ++k)
-                v[k] = make_uint4(two(c + 8 * k), two(c + 8 * k + 2), two(c + 8 * k + 4), two(c + 8 * k + 6));
-            store_rows<CH>(v, o0 + c0 + c, sizeof(bf16) * p.out_cols, n, stage, lane, (cols - c0 - c) / 8);
-        }
+        for (int k = 0; k < 4; ++k)
+            v[k] = make_uint4(two(8 * k), two(8 * k + 2), two(8 * k + 4), two(8 * k + 6));
+        store_rows64(v, o0 + c0, sizeof(bf16) * p.out_cols, n, stage, lane, (cols - c0) / 8);
     }
 }
 
-// down rows for a sum over a token's experts by a later kernel: blocks of 64 columns of
-// v = w * product as 16-bit integers with the scale max |v| / 32767.  As many bytes as bf16 rows,
-// but an error of 2^-16 of the block's largest value instead of 2^-9 of each: bf16 rows would
-// add as much again to the error of the bf16 result.  fp32 reductions into the tokens' rows (1 GB
-// of them at 65536 x 4096) kept the tensor cores waiting: 454 us.
-constexpr int kRows16Block = 64;
-template <int CH>
+// down rows for a sum over a token's experts by a later kernel: blocks of 32 columns of the
+// products as 16-bit integers with the scale max |product| / 32767 (times the row's factor w).
+// Nearly as few bytes as bf16 rows, but an error of 2^-16 of the block's largest value instead of
+// 2^-9 of each: bf16 rows would add as much again to the error of the bf16 result.  fp32
+// reductions into the tokens' rows (1 GB of them at 65536 x 4096) kept the tensor cores
+// waiting: 454 us.
+constexpr int kRows16Block = 32;
 __device__ __forceinline__ void i8_rows16_epilogue(const Params& p, uint32_t tcol, int row0, int n,
-                                                   float w, int col0, int hc, const float* scales,
-                                                   float* stage, int lane) {
+                                                   float w, int col0, const float* scales, float* stage,
+                                                   int lane) {
     constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to the low bits
     int16_t* y0 = p.y16q_out + static_cast<size_t>(row0) * p.out_cols + col0;
-    float* s0 = p.y16q_scale + static_cast<size_t>(row0 + lane) * (p.out_cols / kRows16Block) +
-                col0 / kRows16Block;
-#pragma unroll 1
-    for (int b0 = 0; b0 < hc; b0 += kRows16Block) {
-        uint32_t v[2][32];
-        tmem_ld32(tcol + b0, v[0]);
-        tmem_ld32(tcol + b0 + 32, v[1]);
-        tmem_ld_wait();
-        // the row's factor w goes into the block's scale
+    float block_scale[4];
+    uint32_t v[2][32];  // a block in work, the next one on its way from tensor memory
+    tmem_ld32(tcol, v[0]);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        uint32_t(&t)[32] = v[b & 1];
+        tmem_ld_wait_dep(t);
+        if (b + 1 < 4) tmem_ld32(tcol + (b + 1) * kRows16Block, v[(b + 1) & 1]);
+        scale_columns<32>(t, scales + b * kRows16Block);
         float top = 0.f;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            scale_columns<32>(v[c], scales + b0 + 32 * c);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) top = fmaxf(top, fabsf(__uint_as_float(v[c][j])));
-        }
+        for (int j = 0; j < 32; ++j) top = fmaxf(top, fabsf(__uint_as_float(t[j])));
         const bool any = top > 1e-30f && top < INFINITY;
         const float inv = any ? __fdividef(32767.f, top) : 0.f;
         // (a NaN comes in by w; products that overflow make their block NaN)
-        if (lane < n) s0[b0 / kRows16Block] = any ? w * (top * (1.f / 32767.f)) : w * (top < 1.f ? 0.f : NAN);
+        block_scale[b] = any ? w * (top * (1.f / 32767.f)) : w * (top < 1.f ? 0.f : NAN);
+        auto two = [&](int j) {
+            return __byte_perm(__float_as_uint(fmaf(__uint_as_float(t[j]), inv, kMagic)),
+                               __float_as_uint(fmaf(__uint_as_float(t[j + 1]), inv, kMagic)), 0x5410);
+        };
+        uint4 o[4];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            auto two = [&](int j) {
-                return __byte_perm(__float_as_uint(fmaf(__uint_as_float(v[c][j]), inv, kMagic)),
-                                   __float_as_uint(fmaf(__uint_as_float(v[c][j + 1]), inv, kMagic)), 0x5410);
-            };
-#pragma unroll
-            for (int d = 0; d < 32; d += 8 * CH) {
-                uint4 o[CH];
-#pragma unroll
-                for (int k = 0; k < CH; ++k)
-                    o[k] = make_uint4(two(d + 8 * k), two(d + 8 * k + 2), two(d + 8 * k + 4), two(d + 8 * k + 6));
-                store_rows<CH>(o, y0 + b0 + 32 * c + d, sizeof(int16_t) * p.out_cols, n, stage, lane);
-            }
-        }
+        for (int k = 0; k < 4; ++k)
+            o[k] = make_uint4(two(8 * k), two(8 * k + 2), two(8 * k + 4), two(8 * k + 6));
+        store_rows64(o, y0 + b * kRows16Block, sizeof(int16_t) * p.out_cols, n, stage, lane);
     }
+    if (lane < n)
+        *reinterpret_cast<float4*>(p.y16q_scale +
+                                   static_cast<size_t>(row0 + lane) * (p.out_cols / kRows16Block) +
+                                   col0 / kRows16Block) =
+            make_float4(block_scale[0], block_scale[1], block_scale[2], block_scale[3]);
 }
 
 __device__ __forceinline__ int4 add4(int4 a, int4 b) {
@@ -1036,8 +1017,7 @@ __device__ __forceinline__ void i8_split_fixup(const Params& p, int row0, int ro
 // ROWS16: the kernel may write bf16 rows (p.y16_out; the CTA-pair kernel only).
 // I8: int32 accumulators; rs is the row's scale (down: times its weight), scales the warp's
 // column scales.
-// SPLIT: warps that share the tile's columns (2; 4: int8 only).
-template <bool GATE_UP, bool ROWS16 = false, bool I8 = false, int SPLIT = 2>
+template <bool GATE_UP, bool ROWS16 = false, bool I8 = false>
 __device__ __forceinline__ void tm_epilogue(const Params& p, uint32_t tbase, int row, bool valid,
                                             int tile_i, int half, float* stage, int wn,
                                             float* part = nullptr, float rs = 1.f,
@@ -1046,27 +1026,26 @@ __device__ __forceinline__ void tm_epilogue(const Params& p, uint32_t tbase, int
     // few rows in the tile: a warp without any has nothing to drain
     const int n_rows = I8 ? __popc(__ballot_sync(0xffffffffu, valid)) : 0;  // the warp's first rows
     if (I8 && n_rows == 0) return;
-    constexpr int CH = 8 / SPLIT;  // 16-byte chunks that the warp's stage holds of a row
     if (I8 && GATE_UP) {
-        const int F = wn >> 1, hc = F / SPLIT, feat = tile_i * F + half * hc;
+        const int F = wn >> 1, hc = F >> 1, feat = tile_i * F + half * hc;
         if (part) {
             float* prow = part + static_cast<size_t>(row) * 2 * p.out_cols + feat;
             i8_store_partials(tbase + half * hc, prow, hc, valid);
             i8_store_partials(tbase + F + half * hc, prow + p.out_cols, hc, valid);
         } else {
-            i8_gate_up_epilogue<CH>(p, tbase + half * hc, tbase + F + half * hc, row - lane, n_rows, rs,
+            i8_gate_up_epilogue(p, tbase + half * hc, tbase + F + half * hc, row - lane, n_rows, rs,
                                 feat, hc, scales, stage, lane);
         }
     } else if (I8 && p.dense) {
         // dense product; the last tile may hold fewer than wn columns
-        const int hc = wn / SPLIT, col0 = tile_i * wn + half * hc;
+        const int hc = wn >> 1, col0 = tile_i * wn + half * hc;
         const int cols = min(hc, p.out_cols - col0);
         if (cols <= 0) return;
         if (part)
             i8_store_partials(tbase + half * hc, part + static_cast<size_t>(row) * p.out_cols + col0,
                               cols, valid);
         else
-            i8_dense_epilogue<CH>(p, tbase + half * hc, row - lane, n_rows, rs, col0, cols, scales, stage,
+            i8_dense_epilogue(p, tbase + half * hc, row - lane, n_rows, rs, col0, cols, scales, stage,
                               lane);
     } else if (GATE_UP && part) {
         // one K slice of the tile: fp32 partial sums of the gate and up features
@@ -1115,13 +1094,13 @@ __device__ __forceinline__ void tm_epilogue(const Params& p, uint32_t tbase, int
             if (valid) swiglu_store16(gv, uv, hrow);
         }
     } else {
-        const int hc = wn / SPLIT;  // output columns of this warp
+        const int hc = wn >> 1;  // output columns of this warp: 128, 64 or 32
         // the last tile of an int8 launch may hold half the columns (out_cols is a multiple
         // of 128, the tile of 256)
         if (I8 && tile_i * wn + half * hc >= p.out_cols) return;
         if (I8 && ROWS16 && p.y16q_out) {
-            i8_rows16_epilogue<CH>(p, tbase + half * hc, row - lane, n_rows, rs, tile_i * wn + half * hc,
-                                   hc, scales, stage, lane);
+            i8_rows16_epilogue(p, tbase + half * hc, row - lane, n_rows, rs, tile_i * wn + half * hc,
+                               scales, stage, lane);
             return;
         }
         const float w = I8 ? rs : (valid && p.sorted_w) ? __ldg(p.sorted_w + row) : 1.f;
@@ -1211,17 +1190,11 @@ __device__ __forceinline__ float* epi_stage(int* table_end, int warp) {
     return reinterpret_cast<float*>(a) + (warp - 2) * kStageFloatsPerWarp;
 }
 
-// int8 kernels: a warp's 2 KB (SPLIT 2) or 1 KB of staging, and after all warps' its column
-// scales
-template <int SPLIT>
-__device__ __forceinline__ float* i8_stage(int* table_end, int warp) {
-    return epi_stage(table_end, 2) + (warp - 2) * (2 * kStageFloatsPerWarp / SPLIT);
-}
-template <int SPLIT>
+// int8 kernels: after the staging, the epilogue warps' column scales (kTmN / 2 floats each)
 __device__ __forceinline__ float* i8_scales(int* table_end, int warp) {
-    return epi_stage(table_end, 2) + 8 * kStageFloatsPerWarp + (warp - 2) * (kTmN / SPLIT);
+    return epi_stage(table_end, 2) + 8 * kStageFloatsPerWarp + (warp - 2) * (kTmN / 2);
 }
-constexpr size_t kScaleBytes = 4 * kTmN * sizeof(float);
+constexpr size_t kI8EpilogueBytes = kEpiStageBytes + 8 * (kTmN / 2) * sizeof(float);
 
 // A tile's scales for one epilogue warp: its lane's row -- gate_up and dense the token's scale,
 // down the row's own and its routing weight -- and four columns.  `index` is where the row's
@@ -1233,13 +1206,13 @@ struct TileScales {
     float4 col;
     __device__ __forceinline__ float factor() const { return row * weight; }
 };
-template <bool GATE_UP, int WN, int SPLIT>
+template <bool GATE_UP, int WN>
 __device__ __forceinline__ TileScales tile_scales(const Params& p, const Tile& t, int row_in_tile, int half,
                                                   int lane) {
     const int row = t.row0 + row_in_tile;
     const bool in = row < t.row_end;
     TileScales s;
-    s.col = load_scales<GATE_UP, WN, SPLIT>(p, t.g * p.w_group_rows + t.i * (GATE_UP ? WN / 2 : WN),
+    s.col = load_scales<GATE_UP, WN>(p, t.g * p.w_group_rows + t.i * (GATE_UP ? WN / 2 : WN),
                                             t.i * WN, half, lane);
     s.index = !in ? -1 : p.scale_tok ? __ldg(p.scale_tok + row) : row;
     s.weight = !GATE_UP && in && p.sorted_w ? __ldg(p.sorted_w + row) : 1.f;
@@ -1432,11 +1405,11 @@ grouped_gemm_tm_kernel(const __grid_constant__ CUtensorMap map_w,
         const int q = warp & 3;
         if (GATE_UP) clear_accumulator(p, threadIdx.x - 64, kTmEpiThreads);
         const int half = (warp - 2) >> 2;
-        float* scales = I8 ? i8_scales<2>(g_tile + p.G + 1, warp) : nullptr;
+        float* scales = I8 ? i8_scales(g_tile + p.G + 1, warp) : nullptr;
         uint32_t abuf = 0, aphase = 0;
         TileScales next{};
         if (I8 && static_cast<int>(blockIdx.x) < total) {
-            next = tile_scales<GATE_UP, WN, 2>(
+            next = tile_scales<GATE_UP, WN>(
                 p, decode_tile(unit_at(units, blockIdx.x).tile, g_tile, g_off, p.G, kTmRows), q * 32 + lane,
                 half, lane);
             tile_row_scale(p, next);
@@ -1452,7 +1425,7 @@ grouped_gemm_tm_kernel(const __grid_constant__ CUtensorMap map_w,
                 put_scales<WN / 8>(scales, now.col, lane);
                 const int after = tile + static_cast<int>(gridDim.x);
                 if (after < total)
-                    next = tile_scales<GATE_UP, WN, 2>(
+                    next = tile_scales<GATE_UP, WN>(
                         p, decode_tile(unit_at(units, after).tile, g_tile, g_off, p.G, kTmRows),
                         q * 32 + lane, half, lane);
             }
@@ -1531,9 +1504,8 @@ struct CfgPair {
     static constexpr int kPairRows = 2 * kTmRows;  // token rows per pair tile
 };
 
-// SPLIT: epilogue warps that share a tile's columns; 4 SPLIT epilogue warps in all (8 for bf16).
-template <bool GATE_UP, bool I8 = false, int SPLIT = 2>
-__global__ void __launch_bounds__(64 + 128 * SPLIT, 1)
+template <bool GATE_UP, bool I8 = false>
+__global__ void __launch_bounds__(kTmThreads, 1)
 grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w,
                          const __grid_constant__ CUtensorMap map_act, Params p) {
     using C = CfgPair;
@@ -1563,7 +1535,7 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w,
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);    // both: the leader's multicast commit
-            mbar_init(&tempty[b], 8 * SPLIT);  // leader: the epilogue warps of both CTAs
+            mbar_init(&tempty[b], 16);  // leader: the 8 epilogue warps of each CTA
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -1680,15 +1652,15 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w,
     } else {
         // ---------------------------------------------------------------- epilogue (both)
         const int q = warp & 3;
-        if (GATE_UP) clear_accumulator(p, threadIdx.x - 64, 128 * SPLIT);
+        if (GATE_UP) clear_accumulator(p, threadIdx.x - 64, kTmEpiThreads);
         const uint32_t leader_tempty0 = map_to_rank(smem_u32(&tempty[0]), 0);
         const int half = (warp - 2) >> 2;
         const int row_in_tile = static_cast<int>(rank) * kTmRows + q * 32 + lane;
-        float* scales = I8 ? i8_scales<SPLIT>(g_tile + p.G + 1, warp) : nullptr;
+        float* scales = I8 ? i8_scales(g_tile + p.G + 1, warp) : nullptr;
         uint32_t abuf = 0, aphase = 0;
         TileScales next{};
         if (I8 && pair < total) {
-            next = tile_scales<GATE_UP, kTmN, SPLIT>(
+            next = tile_scales<GATE_UP, kTmN>(
                 p, decode_tile(pair, g_tile, g_off, p.G, C::kPairRows), row_in_tile, half, lane);
             tile_row_scale(p, next);
         }
@@ -1697,9 +1669,9 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w,
             const int row = t.row0 + row_in_tile;
             const TileScales now = next;
             if (I8) {
-                put_scales<kTmN / SPLIT / 4>(scales, now.col, lane);
+                put_scales<kTmN / 8>(scales, now.col, lane);
                 if (tile + npairs < total)
-                    next = tile_scales<GATE_UP, kTmN, SPLIT>(
+                    next = tile_scales<GATE_UP, kTmN>(
                         p, decode_tile(tile + npairs, g_tile, g_off, p.G, C::kPairRows), row_in_tile, half,
                         lane);
             }
@@ -1716,12 +1688,9 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_w,
             tc_fence_after();
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    abuf * C::kAccCols;
-            tm_epilogue<GATE_UP, true, I8, SPLIT>(
+            tm_epilogue<GATE_UP, true, I8>(
                 p, tbase, row, row < t.row_end, t.i, half,
-                I8        ? i8_stage<SPLIT>(g_tile + p.G + 1, warp)
-                : GATE_UP ? nullptr
-                          : epi_stage(g_tile + p.G + 1, warp),
-                kTmN, nullptr, I8 ? now.factor() : 1.f, scales);
+                GATE_UP && !I8 ? nullptr : epi_stage(g_tile + p.G + 1, warp), kTmN, nullptr, I8 ? now.factor() : 1.f, scales);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {

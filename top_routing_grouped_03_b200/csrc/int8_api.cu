@@ -118,7 +118,7 @@ void take_experts(Taker& take, ExpertsLayout& L, long long T, long long D, long 
     L.acc = take(sizeof(float) * T * D);
     // rows for a sum by the combine: fp32 (fixed order), 16-bit integers and scales (CTA pairs)
     L.y = take(det ? sizeof(float) * rows * D : pairs ? sizeof(int16_t) * rows * D : 0);
-    L.y_scale = take(!det && pairs ? sizeof(float) * rows * (D / 64) : 0);
+    L.y_scale = take(!det && pairs ? sizeof(float) * rows * (D / 32) : 0);
     L.part = take(gate_up_split_ok(T, K, f) ? sizeof(float) * kSplitMax * rows * 2 * f : 0);
 }
 ExpertsLayout experts_layout(long long T, long long D, long long E, long long K, long long f,

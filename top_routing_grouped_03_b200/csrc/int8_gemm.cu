@@ -67,22 +67,21 @@ int tile_width(const Int8GemmLaunch& a, int num_sms) {
     return 64;
 }
 
-constexpr int kPairSplit = 2;
-
 template <bool GATE_UP>
 cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const Params& p, bool pair, int wn,
                        int ctas, cudaStream_t s, bool pdl) {
-    const size_t ring = pair        ? static_cast<size_t>(CfgPair::kStages) * CfgPair::kStageBytes
-                        : wn == 256 ? static_cast<size_t>(CfgTm<256>::kStages) * CfgTm<256>::kStageBytes
-                        : wn == 128 ? static_cast<size_t>(CfgTm<128>::kStages) * CfgTm<128>::kStageBytes
-                                    : static_cast<size_t>(CfgTm<64>::kStages) * CfgTm<64>::kStageBytes;
-    const int stages = pair        ? CfgPair::kStages
+    using P = CfgPair;
+    const int stages = pair        ? P::kStages
                        : wn == 256 ? CfgTm<256>::kStages
                        : wn == 128 ? CfgTm<128>::kStages
                                    : CfgTm<64>::kStages;
-    const size_t smem = 1024 + ring + (2 * stages + 5) * 8 + 16 + 2 * (p.G + 1) * sizeof(int) +
-                        kEpiStageBytes + kScaleBytes;
-    auto kfn = pair        ? grouped_gemm_pair_kernel<GATE_UP, true, kPairSplit>
+    const int stage_bytes = pair        ? P::kStageBytes
+                            : wn == 256 ? CfgTm<256>::kStageBytes
+                            : wn == 128 ? CfgTm<128>::kStageBytes
+                                        : CfgTm<64>::kStageBytes;
+    const size_t smem = 1024 + static_cast<size_t>(stages) * stage_bytes + (2 * stages + 5) * 8 + 16 +
+                        2 * (p.G + 1) * sizeof(int) + kI8EpilogueBytes;
+    auto kfn = pair        ? grouped_gemm_pair_kernel<GATE_UP, true>
                : wn == 256 ? grouped_gemm_tm_kernel<GATE_UP, true, 256>
                : wn == 128 ? grouped_gemm_tm_kernel<GATE_UP, true, 128>
                            : grouped_gemm_tm_kernel<GATE_UP, true, 64>;
@@ -90,7 +89,7 @@ cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const Param
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(pair ? 64 + 128 * kPairSplit : kTmThreads);
+    cfg.blockDim = dim3(kTmThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
