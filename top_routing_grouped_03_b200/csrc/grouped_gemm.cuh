@@ -1407,27 +1407,20 @@ grouped_gemm_tm_kernel(const __grid_constant__ CUtensorMap map_w,
         const int half = (warp - 2) >> 2;
         float* scales = I8 ? i8_scales(g_tile + p.G + 1, warp) : nullptr;
         uint32_t abuf = 0, aphase = 0;
-        TileScales next{};
-        if (I8 && static_cast<int>(blockIdx.x) < total) {
-            next = tile_scales<GATE_UP, WN>(
-                p, decode_tile(unit_at(units, blockIdx.x).tile, g_tile, g_off, p.G, kTmRows), q * 32 + lane,
-                half, lane);
-            tile_row_scale(p, next);
-        }
         for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
             const Unit un = unit_at(units, tile);
             const Tile t = decode_tile(un.tile, g_tile, g_off, p.G, kTmRows);
             const int row = t.row0 + q * 32 + lane;
             const bool valid = row < t.row_end;
             const int wr = t.g * p.w_group_rows + t.i * (GATE_UP ? WN / 2 : WN);
-            const TileScales now = next;
-            if (I8) {
+            // int8: the tile's scales, loaded while its products are summed (one tile ahead, as in
+            // the CTA-pair kernel, costs the short tiles of a decode batch more than it hides:
+            // 64 tokens, 256 experts 140 against 134 us); warps without rows need none
+            TileScales now{};
+            if (I8 && __ballot_sync(0xffffffffu, valid) != 0) {
+                now = tile_scales<GATE_UP, WN>(p, t, q * 32 + lane, half, lane);
+                tile_row_scale(p, now);
                 put_scales<WN / 8>(scales, now.col, lane);
-                const int after = tile + static_cast<int>(gridDim.x);
-                if (after < total)
-                    next = tile_scales<GATE_UP, WN>(
-                        p, decode_tile(unit_at(units, after).tile, g_tile, g_off, p.G, kTmRows),
-                        q * 32 + lane, half, lane);
             }
             const bool ready = mbar_wait(&tfull[abuf], aphase, kWaitBudgetNs, abort_flag);
             if (!epilogue_bar_and<kTmEpiThreads>(ready)) {
@@ -1449,7 +1442,6 @@ grouped_gemm_tm_kernel(const __grid_constant__ CUtensorMap map_w,
                 p, tbase, row, valid, t.i, half,
                 GATE_UP && !I8 ? nullptr : epi_stage(g_tile + p.G + 1, warp), WN, part,
                 I8 ? now.factor() : 1.f, scales);
-            if (I8) tile_row_scale(p, next);
             tc_fence_before();
             mbar_arrive(&tempty[abuf]);
             abuf ^= 1u;
