@@ -374,7 +374,14 @@ struct RowGather {
     }
 };
 
-template <int BN, bool GATE_UP>
+// SiLU(g) u of a row: the gate and up products, scaled by their weight rows, and the row's scale.
+__device__ __forceinline__ float swiglu_scaled(float gate, float up, float row_scale) {
+    const float g = gate * row_scale, u = up * row_scale;
+    return __fdividef(g, 1.f + __expf(-g)) * u;
+}
+
+// I8: 8-bit operands (not cut into slices; h in fp32, as in the other int8 kernels).
+template <int BN, bool GATE_UP, bool I8 = false>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w,
                     const __grid_constant__ CUtensorMap map_act, Params p) {
@@ -507,7 +514,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w,
                 }
                 tc_fence_after();
                 const uint32_t d0 = tmem_base + abuf * C::kAccCols;
-                constexpr uint32_t idesc = idesc_bf16_f32(kBM, BN);
+                constexpr uint32_t idesc = I8 ? idesc_i8_s32(kBM, BN) : idesc_bf16_f32(kBM, BN);
                 const Unit un = unit_at(units, tile);
                 const int nks = slice_begin(p.nk, un.nsl, un.slice + 1) -
                                 slice_begin(p.nk, un.nsl, un.slice);
@@ -527,8 +534,14 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w,
                     for (int s = 0; s < kBK / 16; ++s) {
                         const uint32_t acc = (kk | s) != 0 ? 1u : 0u;
                         const uint64_t bd = sdesc_k_sw128(b0 + s * 32);
-                        umma_bf16(d0, sdesc_k_sw128(a0 + s * 32), bd, idesc, acc);
-                        if (GATE_UP) umma_bf16(d0 + BN, sdesc_k_sw128(a1 + s * 32), bd, idesc, acc);
+                        const uint64_t ad = sdesc_k_sw128(a0 + s * 32);
+                        if (I8) umma_i8(d0, ad, bd, idesc, acc);
+                        else umma_bf16(d0, ad, bd, idesc, acc);
+                        if (GATE_UP) {
+                            const uint64_t ud = sdesc_k_sw128(a1 + s * 32);
+                            if (I8) umma_i8(d0 + BN, ud, bd, idesc, acc);
+                            else umma_bf16(d0 + BN, ud, bd, idesc, acc);
+                        }
                     }
                     issued = true;
                     umma_commit(&empty[stage]);
@@ -560,6 +573,27 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w,
                               ? p.part + static_cast<size_t>(un.slice) * p.part_rows * 2 * p.out_cols
                               : nullptr;
             const int nsplit = un.nsl;
+            // int8: this thread's weight row's scales, and lane c's row c of each 16 (its scale, times
+            // the routing weight for down, and its token)
+            float cs = 0.f, cs_up = 0.f, row_factor[(BN + 31) / 32];
+            int row_token[(BN + 31) / 32];
+            if (I8) {
+                const int wr = t.g * p.w_group_rows + t.i * kBM + feat_in_tile;
+                cs = __ldg(p.col_scale + wr);
+                if (GATE_UP) cs_up = __ldg(p.col_scale + wr + p.up_rows);
+#pragma unroll
+                for (int b = 0; b < (BN + 31) / 32; ++b) {
+                    const int r = t.row0 + b * 32 + lane;
+                    row_factor[b] = 0.f;
+                    row_token[b] = 0;
+                    if (r < t.row_end && b * 32 + lane < BN) {
+                        const int tok = p.sorted_token ? __ldg(p.sorted_token + r) : r;
+                        row_token[b] = tok;
+                        row_factor[b] = __ldg(p.row_scale + (p.scale_tok ? tok : r));
+                        if (!GATE_UP && p.sorted_w) row_factor[b] *= __ldg(p.sorted_w + r);
+                    }
+                }
+            }
             const bool ready = mbar_wait(&tfull[abuf], aphase, kWaitBudgetNs, abort_flag);
             if (!epilogue_bar_and(ready)) {
                 set_status(p.status, MOE_ERR_TIMEOUT);
@@ -581,6 +615,22 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w,
                 for (int c = 0; c < 16; ++c) {
                     const int row = t.row0 + c0 + c;
                     if (row >= t.row_end) break;
+                    if (I8) {
+                        // (rows of a tile are a prefix: every lane takes the same branches)
+                        const float rs = __shfl_sync(0xffffffffu, row_factor[(c0 + c) / 32], (c0 + c) & 31);
+                        const float v = __int2float_rn(static_cast<int>(gv[c])) * cs;
+                        if (GATE_UP) {
+                            p.h32_out[static_cast<size_t>(row) * p.out_cols + feat] = swiglu_scaled(
+                                v, __int2float_rn(static_cast<int>(uv[c])) * cs_up, rs);
+                        } else {
+                            const int tok =
+                                __shfl_sync(0xffffffffu, row_token[(c0 + c) / 32], (c0 + c) & 31);
+                            if (p.acc_out)
+                                red_add_f32(p.acc_out + static_cast<size_t>(tok) * p.out_cols + feat, rs * v);
+                            if (y_slice) y_slice[static_cast<size_t>(row) * p.out_cols + feat] = rs * v;
+                        }
+                        continue;
+                    }
                     const float g = __uint_as_float(gv[c]);
                     if (GATE_UP && part) {
                         float* pr = part + static_cast<size_t>(row) * 2 * p.out_cols;
@@ -794,11 +844,6 @@ __device__ __forceinline__ void scale_columns(uint32_t* v, const float* cs) {
         v[j + 2] = __float_as_uint(__int2float_rn(static_cast<int>(v[j + 2])) * c.z);
         v[j + 3] = __float_as_uint(__int2float_rn(static_cast<int>(v[j + 3])) * c.w);
     }
-}
-
-__device__ __forceinline__ float swiglu_scaled(float gate, float up, float row_scale) {
-    const float g = gate * row_scale, u = up * row_scale;
-    return __fdividef(g, 1.f + __expf(-g)) * u;
 }
 
 __device__ __forceinline__ float row_scale_of(const Params& p, int row) {

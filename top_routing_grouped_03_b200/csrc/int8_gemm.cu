@@ -5,9 +5,9 @@
 // scales are applied once per element in the epilogue.
 //
 // Against bf16 a weight takes half the bytes (what bounds few tokens: HBM) and the tensor
-// cores do twice the products (what bounds many tokens).  Tokens on M throughout: one-CTA
-// tiles of 128 tokens x 256 weight rows, K cut into slices when the tiles cannot fill the GPU,
-// and CTA pairs (256 x 256) once groups average 128 rows, as for bf16.
+// cores do twice the products (what bounds many tokens).  Weights on M for groups of a handful
+// of rows, one-CTA tiles of 128 tokens x 256 weight rows above (K cut into slices when the
+// tiles cannot fill the GPU), CTA pairs (256 x 256) once groups average 128 rows.
 //
 // gate_up leaves h in fp32: its row maxima are known only when all feature blocks are done.
 // (Letting the CTA that completes a row block quantise it, from L2, saved a launch but was bound
@@ -65,6 +65,31 @@ int tile_width(const Int8GemmLaunch& a, int num_sms) {
     for (int wn = kTmN; wn > 64; wn /= 2)
         if (2 * blocks * ceil_div(cols, wn) > num_sms) return wn;
     return 64;
+}
+
+// Weights on M (128 weight rows x 32 token rows) while the groups average a handful of rows: all
+// epilogue warps then have features to drain, where a 128-row tile of tokens leaves the two
+// or three rows of a group to one quarter of them (64 tokens, 256 experts, 8 each: 134.8 with tokens
+// on M, 130.8 us; 8 tokens, 128 experts of 1024 x 4096: 165 to 134 us; 16-row tiles the same).
+// Above, and with skewed routing, tokens on M read hot experts' weights fewer times (300 tokens,
+// 9 rows a group on average, Zipf: 43 against 56 us).
+constexpr int kSwapRows = 32;
+bool use_swap(const Int8GemmLaunch& a) {
+    return a.kind != Int8GemmLaunch::kDense && a.E > 1 && a.rows / a.E <= 8;
+}
+
+template <bool GATE_UP>
+cudaError_t launch_swap(const CUtensorMap& mw, const CUtensorMap& ma, const Params& p, int ctas,
+                        cudaStream_t s, bool pdl) {
+    using C = Cfg<kSwapRows, GATE_UP>;
+    const size_t smem = 1024 + static_cast<size_t>(C::kStages) * C::kStageBytes + (2 * C::kStages + 5) * 8 +
+                        16 + 2 * (p.G + 1) * sizeof(int);
+    auto kfn = grouped_gemm_kernel<kSwapRows, GATE_UP, true>;
+    cudaError_t err = set_smem_limit(reinterpret_cast<const void*>(kfn), smem);
+    if (err != cudaSuccess) return err;
+    err = launch_kernel(kfn, dim3(ctas), dim3(kThreads), smem, s, pdl, mw, ma, p);
+    count_launches(1);
+    return err;
 }
 
 template <bool GATE_UP>
@@ -140,12 +165,13 @@ cudaError_t launch_int8_gemm(const Int8GemmLaunch& a, int num_sms, cudaStream_t 
         pdl = true;
     }
     CUtensorMap mw, ma;
-    const int wn = pair ? kTmN : tile_width(a, num_sms);
-    if ((err = encode_tile_map(&mw, a.w, static_cast<uint64_t>(w_group_rows) * a.E, K / 2, wn / 2)) !=
+    const bool swap = !pair && use_swap(a);
+    const int wn = pair || swap ? kTmN : tile_width(a, num_sms);
+    if ((err = encode_tile_map(&mw, a.w, static_cast<uint64_t>(w_group_rows) * a.E, K / 2, swap ? kBM : wn / 2)) !=
         cudaSuccess)
         return err;
     // with a gather the activation map is not read: it covers the first row
-    if ((err = encode_tile_map(&ma, act, gather ? 1 : a.rows, K / 2, gather ? 1 : kTmRows)) != cudaSuccess)
+    if ((err = encode_tile_map(&ma, act, gather ? 1 : a.rows, K / 2, gather ? 1 : swap ? kSwapRows : kTmRows)) != cudaSuccess)
         return err;
     Params p{};
     p.offsets = a.offsets;
@@ -153,7 +179,7 @@ cudaError_t launch_int8_gemm(const Int8GemmLaunch& a, int num_sms, cudaStream_t 
     p.sorted_token = a.sorted_token;
     p.sorted_w = a.sorted_w;
     p.G = a.E;
-    p.nf = gate_up ? a.f / (wn / 2) : ceil_div(a.D, wn);
+    p.nf = swap ? (gate_up ? a.f : a.D) / kBM : gate_up ? a.f / (wn / 2) : ceil_div(a.D, wn);
     p.nk = ceil_div(K, 2 * kBK);
     p.w_group_rows = w_group_rows;
     p.up_rows = a.f;
@@ -167,6 +193,7 @@ cudaError_t launch_int8_gemm(const Int8GemmLaunch& a, int num_sms, cudaStream_t 
     p.gather_tok = gather ? a.sorted_token : nullptr;
     p.x = reinterpret_cast<const bf16*>(act);
     p.ksplit = 1;
+    p.act_box = kSwapRows;
     p.zero_acc = gate_up ? a.zero_acc : nullptr;
     p.zero_n4 = a.zero_floats / 4;
     p.row_scale = a.act_scale;
@@ -175,7 +202,7 @@ cudaError_t launch_int8_gemm(const Int8GemmLaunch& a, int num_sms, cudaStream_t 
     p.h32_out = a.h_out;
     p.dense = dense ? 1 : 0;
     // gate_up and dense slices meet in the partial-sum planes; down's add into acc_out
-    const bool split = !pair && a.ksplit_max > 1 &&
+    const bool split = !pair && !swap && a.ksplit_max > 1 &&
                        (a.kind == Int8GemmLaunch::kDown
                             ? (a.acc_out != nullptr && a.y_out == nullptr && a.y16_out == nullptr)
                             : (a.part != nullptr && a.tickets != nullptr && a.ticket_cap > 0));
@@ -188,11 +215,13 @@ cudaError_t launch_int8_gemm(const Int8GemmLaunch& a, int num_sms, cudaStream_t 
     p.tickets = a.tickets;
     p.ticket_cap = a.ticket_cap;
     // persistent: one CTA (or pair) per SM, fewer when the units cannot fill them
-    const int tile_rows = pair ? CfgPair::kPairRows : kTmRows;
+    const int tile_rows = pair ? CfgPair::kPairRows : swap ? kSwapRows : kTmRows;
     const long long max_tiles = (static_cast<long long>(ceil_div(a.rows, tile_rows)) +
                                  std::min(p.G, a.rows)) * p.nf * p.ksplit_max;
     const int ctas = pair ? 2 * static_cast<int>(std::min<long long>(max_tiles, num_sms / 2))
                           : static_cast<int>(std::min<long long>(max_tiles, num_sms));
+    if (swap) return gate_up ? launch_swap<true>(mw, ma, p, ctas, s, pdl)
+                             : launch_swap<false>(mw, ma, p, ctas, s, pdl);
     return gate_up ? launch_one<true>(mw, ma, p, pair, wn, ctas, s, pdl)
                    : launch_one<false>(mw, ma, p, pair, wn, ctas, s, pdl);
 }
