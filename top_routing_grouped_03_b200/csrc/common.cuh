@@ -152,7 +152,8 @@ struct RouteLogitsLaunch {
     float* topk_w;
     int32_t* counts;          // [E] overwritten, or NULL
     // filled in by the launcher
-    int group_lanes, group_magic, whole_registers;
+    int group_size, group_magic, group_lpg, group_shift, group_pad, whole_registers,
+        speaker_shift;
 };
 cudaError_t launch_route_logits(const RouteLogitsLaunch& a, int num_sms, cudaStream_t s,
                                 bool pdl = false);

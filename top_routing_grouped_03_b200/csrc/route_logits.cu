@@ -19,9 +19,16 @@
 // One warp per token, expert e = 32 j + lane in register j.  Keys are kept as unsigned
 // integers in the order of the floats.  TopK in two steps: the K-th best of the 32 lanes' own
 // maxima bounds the K-th best key from below; the keys that reach it (K to about 2 K of them)
-// are gathered, one to a lane, and each lane counts the ones before its own.  Counting against values broadcast from shared memory is a short chain of independent
-// compares; K rounds of warp-wide maxima were a chain of K times the latency (16381 x 256
-// logits, K = 8: 33 us).
+// are gathered, one to a lane, and each lane counts the ones before its own.  Counting
+// against values broadcast from shared memory is a short chain of independent compares;
+// K rounds of warp-wide maxima over all registers were a chain of K times the latency and
+// four instructions a round and register.  Groups of 32 experts are single registers, judged
+// by warp-wide maxima; others go through shared memory.
+//
+// Bound by instruction issue (two thirds of it used): 16381 x 256 fp32 logits, K = 8, 8 groups,
+// 800 instructions a token, 20.6 us (17 MB, 2.6 us of memory traffic; 34.8 us with K rounds);
+// 4096 x 512, K = 10, 16 groups, bias: 20.0 us (58.9 with K rounds and every doubtful token
+// decided in fp64 from all of its keys); one token 4.9 us.
 #include <algorithm>
 #include <cfloat>
 
@@ -60,6 +67,13 @@ __device__ __forceinline__ float token_logit(const RouteLogitsLaunch& a, long lo
     for (int q = 1; q < a.planes; ++q) r += load_logit(p + q * a.plane_stride);
     if (a.logit_bias) r += __ldg(a.logit_bias + e);
     return clean(r);
+}
+
+// 1 / v to 1 ulp (0 for +inf)
+__device__ __forceinline__ float quick_reciprocal(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 // What two fp32 keys have to differ by for their order to be certain (twice this for scores
@@ -122,33 +136,42 @@ __device__ __noinline__ Exact exact_scores(const RouteLogitsLaunch& a, long long
     return x;
 }
 
-// The groups that stay (a bit each), in fp64.  key: E doubles of this warp's shared memory.
+// The `want` best of the groups in `near` (a bit each), by their scores in fp64; the warp goes
+// through one group at a time, an expert to a lane.
 template <typename T>
-__device__ __noinline__ unsigned exact_groups(const RouteLogitsLaunch& a, long long token,
-                                              double* key, int lane) {
-    const int S = a.E / a.n_group;
+__device__ __noinline__ unsigned exact_groups(const RouteLogitsLaunch& a, long long token, unsigned near,
+                                              int want, int lane) {
+    const int S = a.group_size;
     const Exact x = exact_scores<T>(a, token, lane);
-#pragma unroll 4
-    for (int e = lane; e < a.E; e += 32) key[e] = x.key(a, token_logit<T>(a, token, e), e);
-    __syncwarp();
-    double m1 = -INFINITY, m2 = -INFINITY;
-    if (lane < a.n_group)
-        for (int i = 0; i < S; ++i) keep_two(m1, m2, key[lane * S + i]);
-    const double mine = group_score(m1, m2, a.group_top);
-    int before = 0;  // groups ahead of this lane's
-    for (int g = 0; g < a.n_group; ++g) {
+    double mine = -INFINITY;  // lane g: the score of group g
+    for (unsigned left = near; left; left &= left - 1) {
+        const int g = __ffs(left) - 1;
+        double m1 = -INFINITY, m2 = -INFINITY;
+        for (int i = lane; i < S; i += 32) {
+            const int e = g * S + i;
+            keep_two(m1, m2, x.key(a, token_logit<T>(a, token, e), e));
+        }
+        for (int o = 16; o > 0; o >>= 1) {
+            const double o1 = __shfl_xor_sync(kAll, m1, o), o2 = __shfl_xor_sync(kAll, m2, o);
+            keep_two(m1, m2, o1);
+            keep_two(m1, m2, o2);
+        }
+        if (lane == g) mine = group_score(m1, m2, a.group_top);
+    }
+    int before = 0;  // near groups ahead of this lane's
+    for (unsigned left = near; left; left &= left - 1) {
+        const int g = __ffs(left) - 1;
         const double o = __shfl_sync(kAll, mine, g);
         if (o > mine || (o == mine && g < lane)) ++before;
     }
-    __syncwarp();
-    return __ballot_sync(kAll, lane < a.n_group && before < a.topk_group);
+    return __ballot_sync(kAll, ((near >> lane) & 1u) && before < want);
 }
 
 // TopK in fp64 over every expert of the allowed groups: the expert of slot k into lane k.
 template <typename T>
 __device__ __noinline__ int exact_topk(const RouteLogitsLaunch& a, long long token, double* key,
                                        unsigned allowed, int lane) {
-    const int E = a.E, S = E / a.n_group;
+    const int E = a.E, S = a.group_size;
     const Exact x = exact_scores<T>(a, token, lane);
     for (int e = lane; e < E; e += 32) key[e] = x.order(a, token_logit<T>(a, token, e), e);
     unsigned taken = 0;  // of this lane's experts, by register j = e / 32
@@ -216,47 +239,82 @@ __device__ __forceinline__ int count_larger(const uint64_t* buf, int n, uint64_t
     return rank;
 }
 
-// The groups that stay (a bit each).  sm holds the values that groups are judged by, each group
-// of S padded to S + pad; lpg lanes look through a group.  best, next: scores of the last
-// group that stays and of the first that does not.
-__device__ __forceinline__ unsigned pick_groups(const RouteLogitsLaunch& a, uint32_t* sm, int S, int pad,
-                                                int lpg, uint32_t* best, uint32_t* next, int lane) {
-    const int g = lane >> (31 - __clz(lpg)), sub = lane & (lpg - 1);  // lpg: a power of two
+// The value that a group is judged by, from its two best keys (0: none).
+__device__ __forceinline__ uint32_t judged(const RouteLogitsLaunch& a, uint32_t m1, uint32_t m2) {
+    if (a.group_top == 1) return m1;
+    return ordered(group_score(unordered(m1), m2 ? unordered(m2) : -INFINITY, 2));
+}
+
+// Groups of 32 experts are one register of the warp each: lane g gets what group g is judged by,
+// from one or two warp-wide maxima a group.
+template <int NV>
+__device__ __forceinline__ uint32_t groups_in_registers(const RouteLogitsLaunch& a,
+                                                        const uint32_t (&key)[NV], int lane) {
+    uint32_t m1 = 0u, m2 = 0u;
+#pragma unroll
+    for (int g = 0; g < NV; ++g) {
+        const uint32_t w = __reduce_max_sync(kAll, key[g]);
+        if (lane == g) m1 = w;
+    }
+    if (a.group_top == 2) {
+#pragma unroll
+        for (int g = 0; g < NV; ++g) {  // the best without one lane that holds the best
+            const uint32_t w1 = __shfl_sync(kAll, m1, g);
+            const int who = __ffs(__ballot_sync(kAll, key[g] == w1)) - 1;
+            const uint32_t w = __reduce_max_sync(kAll, lane == who ? 0u : key[g]);
+            if (lane == g) m2 = w;
+        }
+    }
+    return judged(a, m1, m2);
+}
+
+// The same for groups of any size, whose keys are in sm, each group padded: group_lpg lanes (a
+// power of two) look through a group, and all of them get its value.
+__device__ __forceinline__ uint32_t groups_in_memory(const RouteLogitsLaunch& a, const uint32_t* sm,
+                                                     int lane) {
+    const int S = a.group_size, lpg = a.group_lpg;
+    const int g = lane >> a.group_shift, sub = lane & (lpg - 1);
     uint32_t m1 = 0u, m2 = 0u;
     if (g < a.n_group) {
-        const uint32_t* k = sm + g * (S + pad);
-        if ((S & 3) == 0) {
-            for (int i = 4 * sub; i < S; i += 4 * lpg) {
-                const uint4 v = *reinterpret_cast<const uint4*>(k + i);
-                const uint32_t hi = max(v.x, v.y), lo = min(v.x, v.y);
-                const uint32_t hj = max(v.z, v.w), lj = min(v.z, v.w);
-                const uint32_t h = max(hi, hj), l = max(min(hi, hj), hi > hj ? lo : lj);
-                m2 = max(max(min(m1, h), m2), l);
-                m1 = max(m1, h);
-            }
-        } else {
-            for (int i = sub; i < S; i += lpg) keep_two(m1, m2, k[i]);
-        }
+        const uint32_t* k = sm + g * (S + a.group_pad);
+        for (int i = sub; i < S; i += lpg) keep_two(m1, m2, k[i]);
     }
     for (int o = lpg >> 1; o > 0; o >>= 1) {
         const uint32_t o1 = __shfl_xor_sync(kAll, m1, o), o2 = __shfl_xor_sync(kAll, m2, o);
         m2 = max(min(m1, o1), max(m2, o2));
         m1 = max(m1, o1);
     }
-    const bool speaks = g < a.n_group && sub == 0;
-    uint32_t gs = m1;
-    if (a.group_top == 2 && speaks)
-        gs = ordered(group_score(unordered(m1), m2 ? unordered(m2) : -INFINITY, 2));
-    uint64_t* scores = reinterpret_cast<uint64_t*>(sm);
-    const uint64_t mine = with_index(gs, g);
-    __syncwarp();
-    if (speaks) scores[g] = mine;
-    if (lane == 0 && (a.n_group & 1)) scores[a.n_group] = 0u;
-    __syncwarp();
-    const bool stays = speaks && count_larger(scores, a.n_group, mine) < a.topk_group;
-    *best = __reduce_min_sync(kAll, stays ? gs : 0xffffffffu);
-    *next = __reduce_max_sync(kAll, speaks && !stays ? gs : 0u);
-    return __reduce_or_sync(kAll, stays ? 1u << g : 0u);
+    return judged(a, m1, m2);
+}
+
+// The groups that stay (a bit each): gs is what group g is judged by, in the lanes that speak for
+// one.  *near: the groups on either side of the border whose scores are not certain to be on
+// theirs (0: none).
+__device__ __forceinline__ unsigned pick_groups(const RouteLogitsLaunch& a, uint32_t gs, int g, bool speaks,
+                                                bool exact, unsigned* near, int lane) {
+    unsigned allowed = 0;
+    uint32_t left = speaks ? gs : 0u;
+    for (int i = 0; i < a.topk_group; ++i) {
+        // the best one left; equal ones: the lowest lane, which speaks for the lowest group
+        const unsigned who = __ballot_sync(kAll, left == __reduce_max_sync(kAll, left));
+        const int first = __ffs(who) - 1;
+        allowed |= 1u << (first >> a.speaker_shift);
+        if (lane == first) left = 0u;
+    }
+    const bool stays = speaks && left == 0u;
+    *near = 0;
+    if (!exact) {
+        const float last = unordered(__reduce_min_sync(kAll, stays ? gs : 0xffffffffu));
+        const float after = unordered(__reduce_max_sync(kAll, speaks && !stays ? gs : 0u));
+        const float tol = 2.f * uncertain(a, last);
+        if (after > -INFINITY && !(last - after > tol)) {
+            const float v = unordered(gs);
+            *near = __reduce_or_sync(
+                kAll, speaks && (stays ? !(v - after > tol) : v > -INFINITY && !(last - v > tol)) ? 1u << g
+                                                                                                 : 0u);
+        }
+    }
+    return allowed;
 }
 
 // Weights from differences of logits, for scores whose sum (nearly) underflows: there
@@ -274,7 +332,8 @@ __device__ __noinline__ float far_weight(float l) {
 // calls): a launch of few tokens is bound by fetching it.
 template <typename T, int NV, bool SIGMOID, bool SUMS>
 __device__ __forceinline__ void route_token(const RouteLogitsLaunch& a, long long token,
-                                            uint32_t* sm, int* hist, int lane) {
+                                            const float (&bias)[NV], uint32_t* sm, int* hist,
+                                            int lane) {
     const int E = a.E, K = a.K;
     const bool grouped = a.topk_group < a.n_group;
     const bool on_logits = a.select_bias == nullptr;  // the logits have the keys' order
@@ -319,34 +378,34 @@ __device__ __forceinline__ void route_token(const RouteLogitsLaunch& a, long lon
         const float inv_z = __fdividef(1.f, z);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int e = j * 32 + lane;
-            float k = SIGMOID ? __fdividef(1.f, 1.f + __expf(-r[j])) : __expf(r[j] - m) * inv_z;
-            if (!on_logits && e < E) k += __ldg(a.select_bias + e);
+            float k = SIGMOID ? quick_reciprocal(1.f + __expf(-r[j])) : __expf(r[j] - m) * inv_z;
+            k += bias[j];  // (0 without one)
             key[j] = ordered(r[j] > -INFINITY ? fmaxf(k, -INFINITY) : -INFINITY);
         }
     }
     unsigned allowed = kAll;
     if (grouped) {
-        const int S = E / a.n_group, lpg = 32 / a.group_lanes;
-        const int pad = (S & 3) == 0 ? 4 * lpg : lpg;  // keeps the lanes' reads off each other's banks
-        if (a.whole_registers) {  // groups of 32 m experts: one group to a register
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if (j * 32 < E) sm[j * 32 + ((j * 32 * a.group_magic) >> 20) * pad + lane] = key[j];
+        uint32_t gs;
+        int g = lane;
+        bool speaks = lane < a.n_group;
+        if (a.whole_registers) {
+            gs = groups_in_registers<NV>(a, key, lane);
         } else {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int e = j * 32 + lane;
-                if (e < E) sm[e + ((e * a.group_magic) >> 20) * pad] = key[j];
+                if (e < E) sm[e + ((e * a.group_magic) >> 20) * a.group_pad] = key[j];
             }
+            __syncwarp();
+            gs = groups_in_memory(a, sm, lane);
+            g = lane >> a.group_shift;
+            speaks = g < a.n_group && (lane & (a.group_lpg - 1)) == 0;
         }
-        __syncwarp();
-        uint32_t best, next;
-        allowed = pick_groups(a, sm, S, pad, lpg, &best, &next, lane);
-        if (!on_logits || group_sums) {
-            const float last = unordered(best), after = unordered(next);
-            if (after > -INFINITY && !(last - after > 2.f * uncertain(a, last)))
-                allowed = exact_groups<T>(a, token, reinterpret_cast<double*>(sm), lane);
+        unsigned near;
+        allowed = pick_groups(a, gs, g, speaks, on_logits && !group_sums, &near, lane);
+        if (near) {
+            const unsigned sure = allowed & ~near;
+            allowed = sure | exact_groups<T>(a, token, near, a.topk_group - __popc(sure), lane);
         }
         if (on_logits && group_sums) {
 #pragma unroll
@@ -355,7 +414,7 @@ __device__ __forceinline__ void route_token(const RouteLogitsLaunch& a, long lon
         if (a.whole_registers) {
 #pragma unroll
             for (int j = 0; j < NV; ++j)
-                if (!((allowed >> ((j * 32 * a.group_magic) >> 20)) & 1u)) key[j] = 0u;
+                if (!(allowed & (1u << j))) key[j] = 0u;
         } else {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
@@ -459,7 +518,7 @@ __device__ __forceinline__ void route_token(const RouteLogitsLaunch& a, long lon
 }
 
 template <typename T, int NV, bool SIGMOID, bool SUMS>
-__global__ void __launch_bounds__(kThreads, NV <= 8 ? 4 : 3)
+__global__ void __launch_bounds__(kThreads, 4)
 route_logits_kernel(const __grid_constant__ RouteLogitsLaunch a, int warp_bytes) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int hist[512];
@@ -469,9 +528,13 @@ route_logits_kernel(const __grid_constant__ RouteLogitsLaunch a, int warp_bytes)
     __syncthreads();
     grid_dep_wait();
     grid_dep_launch();
+    float bias[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        bias[j] = a.select_bias && j * 32 + lane < a.E ? __ldg(a.select_bias + j * 32 + lane) : 0.f;
     for (long long t = static_cast<long long>(blockIdx.x) * kWarps + warp; t < a.T;
          t += static_cast<long long>(gridDim.x) * kWarps)
-        route_token<T, NV, SIGMOID, SUMS>(a, t, sm, hist, lane);
+        route_token<T, NV, SIGMOID, SUMS>(a, t, bias, sm, hist, lane);
     __syncthreads();
     if (a.counts)
         for (int e = threadIdx.x; e < a.E; e += kThreads) {
@@ -509,16 +572,19 @@ cudaError_t launch_route_logits(const RouteLogitsLaunch& in, int num_sms, cudaSt
     }
     if (a.T == 0 && !a.counts) return cudaSuccess;
     const int S = a.E / a.n_group;
-    a.group_lanes = 1;
-    while (a.group_lanes < a.n_group) a.group_lanes *= 2;
-    a.whole_registers = S % 32 == 0;
+    a.group_size = S;
+    a.whole_registers = S == 32;
     a.group_magic = ((1 << 20) + S - 1) / S;  // e / S = e * magic >> 20 for e < 512
+    a.group_shift = 5;
+    while ((32 >> a.group_shift) < a.n_group) --a.group_shift;
+    a.group_lpg = 1 << a.group_shift;
+    a.speaker_shift = a.whole_registers ? 0 : a.group_shift;
+    a.group_pad = a.group_lpg;  // keeps the lanes' reads off each other's banks
     // a warp's shared memory: the keys by group, each group padded; candidates and slots; the
     // fp64 keys of the rare paths
-    const int lpg = 32 / a.group_lanes;
     size_t warp_bytes = std::max<size_t>(sizeof(uint64_t) * (34 + 18), sizeof(double) * a.E);
     if (a.topk_group < a.n_group)
-        warp_bytes = std::max(warp_bytes, sizeof(uint32_t) * (a.E + static_cast<size_t>(a.n_group) * 4 * lpg));
+        warp_bytes = std::max(warp_bytes, sizeof(uint32_t) * (a.E + static_cast<size_t>(a.n_group) * a.group_pad));
     warp_bytes = (warp_bytes + 15) & ~static_cast<size_t>(15);
     const int grid = one ? 1 : static_cast<int>(std::min<long long>(ceil_div(a.T, kWarps), 4ll * num_sms));
     // (bf16 logits are given ones: no planes, no bias)
