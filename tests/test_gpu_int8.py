@@ -156,6 +156,11 @@ CASES = [(1, 2048, 8, 4, 128, None),     # K cut into slices
          (5, 384, 6, 3, 256, None),      # half a tile of output columns
          (64, 256, 16, 4, 128, "few"),
          (200, 256, 4, 2, 384, "one"),   # a hot expert, idle ones
+         (2, 256, 8, 2, 1152, None),     # a handful of rows, by chunks of a weight row
+         (3, 1024, 8, 4, 512, "few"),
+         (1, 384, 4, 3, 640, None),
+         (64, 256, 64, 4, 128, "few"),   # few rows on average, hot experts
+         (24, 2048, 2, 2, 128, None),    # one-CTA tiles cut into slices
          (300, 640, 4, 2, 128, None),    # CTA pairs
          (700, 256, 3, 2, 256, "one")]
 
@@ -181,7 +186,7 @@ def test_no_tokens(moe):
     assert y.shape == (0, 256)
 
 
-@pytest.mark.parametrize("T,E,C", [(40, 8, 5), (600, 4, 150), (600, 4, 0)])
+@pytest.mark.parametrize("T,E,C", [(4, 8, 1), (40, 8, 5), (600, 4, 150), (600, 4, 0)])
 @pytest.mark.parametrize("deterministic", [False, True])
 def test_dropped_rows_add_nothing(moe, oracle_mod, T, E, C, deterministic):
     """An expert capacity leaves rows behind the last group; NaN weights there must not show."""

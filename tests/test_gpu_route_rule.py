@@ -99,6 +99,15 @@ def test_disabled_experts_by_bias(moe):
     assert not ((idx == 5) | (idx == 9)).any() and (idx[:, 0] == 20).all()
 
 
+@pytest.mark.parametrize("G,M", [(1, 1), (4, 2), (2, 1)])
+def test_more_forced_experts_than_slots(moe, G, M):
+    """A bias of +inf for more experts than K: the lowest of them, whatever their scores."""
+    logits, bias = draw(40, 64, 23)
+    bias[10:30] = float("inf")
+    idx, w = check(moe, logits, 6, bias, score="sigmoid", n_group=G, topk_group=M)
+    assert torch.isfinite(w).all() and bool((bias[idx.cpu().long()] == float("inf")).all())
+
+
 def test_far_logits_keep_their_ratios(moe):
     """Sigmoid scores that underflow in fp32 still renormalise to the ratios e^(r_i - r_j)."""
     logits = torch.full((3, 32), -300.0)

@@ -707,5 +707,9 @@ class Int8MoELayer(MoELayer):
             self._ws[:256].zero_()
         return self._ws
 
+    def __call__(self, x, *args, **kw):
+        with torch.cuda.device(x.device):  # (the launches go to the current device)
+            return super().__call__(x, *args, **kw)
+
     def plan(self, T: int):
         raise MoEError(-2, "moe_layer_plan (a layer in 8-bit integers)")

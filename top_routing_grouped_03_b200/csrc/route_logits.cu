@@ -442,7 +442,7 @@ __device__ __forceinline__ void route_token(const RouteLogitsLaunch& a, long lon
     uint32_t low = max(bound, 1u);
     if (!on_logits && bound) {
         const float v = unordered(bound);
-        if (v > -INFINITY) low = ordered(v - uncertain(a, v));
+        if (v > -INFINITY && v < INFINITY) low = ordered(v - uncertain(a, v));
     }
     // candidates to shared memory, lane by lane
     uint64_t* cand = reinterpret_cast<uint64_t*>(sm);
@@ -458,7 +458,7 @@ __device__ __forceinline__ void route_token(const RouteLogitsLaunch& a, long lon
     const int n = __shfl_sync(kAll, at, 31);
     int my_e = 0;
     float l = -INFINITY;  // the slot's logit
-    if (n <= 32) {
+    if (n >= K && n <= 32) {
         at -= own;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
