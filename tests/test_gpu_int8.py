@@ -349,3 +349,46 @@ def test_bf16_layer_with_a_rule(moe):
     from parity import output_error
     err, rms, used = output_error(ref.f64(y), want.cpu().numpy())
     assert used <= 1, (err, rms)
+
+
+# ---------------------------------------------------------------- refusals of the binding
+
+
+def test_binding_refusals(moe):
+    """Shapes, types, strides and devices that do not fit raise before anything is launched."""
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    q, s = torch.zeros(4, 64, dtype=torch.int8, device="cuda"), torch.ones(4, device="cuda")
+    w, ws = torch.zeros(8, 64, dtype=torch.int8, device="cuda"), torch.ones(8, device="cuda")
+    r = torch.zeros(4, 64, device="cuda")
+    for call in (lambda: moe.int8_linear(x, w[:, :32].contiguous(), ws), lambda: moe.int8_linear(x, w, s),
+                 lambda: moe.int8_linear(x[0], w, ws), lambda: moe.int8_matmul(q, ws, w, ws),
+                 lambda: moe.int8_matmul(q, s, w, s), lambda: moe.int8_linear(x, w[:6], ws[:6]),
+                 lambda: moe.int8_linear(x, w, ws, out=torch.empty(4, 9, device="cuda").bfloat16()),
+                 lambda: moe.int8_linear(x[:, :40].contiguous(), w[:, :40].contiguous(), ws),
+                 lambda: moe.quantize_rows(x[:, :40].contiguous()), lambda: moe.route_logits(r, 17),
+                 lambda: moe.route_logits(r, 4, n_group=7), lambda: moe.route_logits(r[0], 4),
+                 lambda: moe.route_logits(r, 9, n_group=8, topk_group=1),
+                 lambda: moe.route_logits(r, 4, select_bias=s),
+                 lambda: moe.route_logits(r, 4, scale=float("nan"))):
+        with pytest.raises(moe.MoEError):
+            call()
+    for call in (lambda: moe.int8_linear(x.float(), w, ws), lambda: moe.int8_linear(x, w.float(), ws),
+                 lambda: moe.quantize_rows(x.half()), lambda: moe.route_logits(r.half(), 4),
+                 lambda: moe.int8_matmul(q, s.double(), w, ws)):
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: moe.int8_linear(x.t().contiguous().t(), w, ws), lambda: moe.int8_linear(x, w.cpu(), ws),
+                 lambda: moe.quantize_rows(x[:, :32]), lambda: moe.route_logits(r[:, ::2], 4),
+                 lambda: moe.int8_matmul(q, s.cpu(), w, ws)):
+        with pytest.raises(ValueError):
+            call()
+    c = Case(6, 256, 4, 2, 128)
+    a = list(c.on_gpu(moe))
+    for i, bad in ((0, a[0][:5].contiguous()), (1, a[1][:5].contiguous()), (2, a[2][:5].contiguous()),
+                   (4, a[4][:3].contiguous()), (5, a[5][:3].contiguous()), (7, a[7][:3].contiguous())):
+        b = list(a)
+        b[i] = bad
+        with pytest.raises(moe.MoEError):
+            moe.experts_int8(*b)
+    with pytest.raises(moe.MoEError):
+        moe.experts_int8(*a, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))

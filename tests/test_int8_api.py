@@ -70,12 +70,13 @@ def test_quantize_refused(lib):
 
 
 def test_int8_matmul_refused(lib):
-    n = lib.moe_int8_workspace_size(4, 64, 64)
-    assert n > 0 and n % 256 == 0
-    for bad in ((4, 60, 64), (4, 64, 60), (-1, 64, 64), (4, 0, 64), (4, 64, 65552), (4, (1 << 20) + 8, 64)):
+    assert lib.moe_int8_workspace_size(8, 64, 64) == 0  # a handful of tokens needs none
+    n = lib.moe_int8_workspace_size(40, 64, 64)
+    assert n > 0 and n % 256 == 0 and lib.moe_int8_workspace_size(4, 64, 32768) > 0
+    for bad in ((40, 60, 64), (40, 64, 60), (-1, 64, 64), (40, 0, 64), (40, 64, 65552), (40, (1 << 20) + 8, 64)):
         assert lib.moe_int8_workspace_size(*bad) == 0, bad
-    mm = [ptr(), ptr(), ptr(), ptr(), 4, 64, 64, ptr(), ptr(), n, None]
-    ln = [ptr(), ptr(), ptr(), 4, 64, 64, ptr(), ptr(), n, None]
+    mm = [ptr(), ptr(), ptr(), ptr(), 40, 64, 64, ptr(), ptr(), n, None]
+    ln = [ptr(), ptr(), ptr(), 40, 64, 64, ptr(), ptr(), n, None]
     for f, ok, cases in (
             (lib.moe_int8_matmul, mm, ((0, None, ARG), (1, None, ARG), (2, None, ARG), (3, None, ARG),
                                        (7, None, ARG), (8, None, WS), (9, n - 1, WS), (5, 60, UNSUP),

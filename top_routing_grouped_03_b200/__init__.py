@@ -367,9 +367,12 @@ def route_logits(logits, K, score="softmax", select_bias=None, n_group=1, topk_g
     T, E = logits.shape
     dev = logits.get_device()
     kind = 0 if logits.dtype is F32 else 1
-    rule = route_rule(E, K, score, select_bias, n_group, topk_group, group_top, renorm, scale)
     if select_bias is not None:
-        _q(select_bias, F32, dev)
+        _need(select_bias.numel() == E, "route_logits (select_bias must be [E])")
+    if group_top is None:
+        group_top = 1 if select_bias is None else 2
+    rule = RouteRule(SCORES[score], _q(select_bias, F32, dev), n_group, topk_group, group_top,
+                     1 if renorm else 0, scale)
     x = _q(logits, F32 if kind == 0 else BF16, dev)
     device = logits.device
     idx = _empty((T, K), (K, 1), dtype=I32, device=device)
@@ -387,25 +390,27 @@ def quantize_rows(x):
     _need(x.dim() >= 1, "quantize_rows (x must have rows)")
     dev = x.get_device()
     p = _q(x, BF16, dev)
-    shape = x.shape
-    q = _empty(shape, x.stride(), dtype=I8, device=x.device)  # (x is contiguous)
-    scale = torch.empty(shape[:-1], dtype=F32, device=x.device)
-    _check(lib().moe_quantize_rows(p, scale.numel(), shape[-1], q.data_ptr(), scale.data_ptr(),
+    shape, stride, device = x.shape, x.stride(), x.device  # (x is contiguous)
+    cols = shape[-1]
+    q = _empty(shape, stride, dtype=I8, device=device)
+    if len(shape) == 2:
+        scale = _empty((shape[0],), (1,), dtype=F32, device=device)
+    else:
+        scale = torch.empty(shape[:-1], dtype=F32, device=device)
+    _check(lib().moe_quantize_rows(p, scale.numel(), cols, q.data_ptr(), scale.data_ptr(),
                                    _raw_stream(dev)), "moe_quantize_rows")
     return q, scale
 
 
 def _int8_buffers(x, T, N, K, out, workspace):
-    n = int(lib().moe_int8_workspace_size(T, N, K))
-    if n == 0:
-        raise MoEError(-2, "moe_int8_workspace_size")
     if out is None:
         out = _empty((T, N), (N, 1), dtype=BF16, device=x.device)
     else:
         _need(out.shape == (T, N), "int8 product (out must be [T, N])")
-    if workspace is None:
-        workspace = _empty((n,), (1,), dtype=U8, device=x.device)
-    return out, workspace
+    if workspace is not None:
+        return out, workspace, workspace.numel()
+    n = int(lib().moe_int8_workspace_size(T, N, K))  # 0: none needed, or an unsupported shape
+    return out, _empty((n,), (1,), dtype=U8, device=x.device) if n else None, n
 
 
 @_on_device_of
@@ -417,8 +422,8 @@ def int8_matmul(xq, x_scale, wq, w_scale, workspace=None, out=None):
     (T, K), N, dev = xq.shape, wq.shape[0], xq.get_device()
     _need(x_scale.shape == (T,) and w_scale.shape == (N,), "int8_matmul (one scale per row)")
     a = _q(xq, I8, dev), _q(x_scale, F32, dev), _q(wq, I8, dev), _q(w_scale, F32, dev)
-    out, ws = _int8_buffers(xq, T, N, K, out, workspace)
-    _check(lib().moe_int8_matmul(*a, T, N, K, _q(out, BF16, dev), _q(ws, U8, dev), ws.numel(),
+    out, ws, n = _int8_buffers(xq, T, N, K, out, workspace)
+    _check(lib().moe_int8_matmul(*a, T, N, K, _q(out, BF16, dev), _q(ws, U8, dev), n,
                                  _raw_stream(dev)), "moe_int8_matmul")
     return out
 
@@ -432,8 +437,8 @@ def int8_linear(x, wq, w_scale, workspace=None, out=None):
     (T, K), N, dev = x.shape, wq.shape[0], x.get_device()
     _need(w_scale.shape == (N,), "int8_linear (one scale per weight row)")
     a = _q(x, BF16, dev), _q(wq, I8, dev), _q(w_scale, F32, dev)
-    out, ws = _int8_buffers(x, T, N, K, out, workspace)
-    _check(lib().moe_int8_linear(*a, T, N, K, _q(out, BF16, dev), _q(ws, U8, dev), ws.numel(),
+    out, ws, n = _int8_buffers(x, T, N, K, out, workspace)
+    _check(lib().moe_int8_linear(*a, T, N, K, _q(out, BF16, dev), _q(ws, U8, dev), n,
                                  _raw_stream(dev)), "moe_int8_linear")
     return out
 
@@ -453,8 +458,8 @@ def experts_int8(xq, x_scale, topk_w, perm, w_gate_up, gate_up_scale, w_down, do
     K, dev = topk_w.shape[1], xq.get_device()
     _need(topk_w.shape[0] == T and w_down.shape[1] == D and w_gate_up.shape == (E, 2 * f, D),
           "experts_int8 (weights and tokens of different shapes)")
-    _need(x_scale.shape == (T,) and gate_up_scale.shape == (E, 2 * f)
-          and down_scale.shape == (E, D), "experts_int8 (one scale per row)")
+    _need(x_scale.numel() == T and gate_up_scale.numel() == 2 * E * f and down_scale.numel() == E * D,
+          "experts_int8 (one scale per row)")
     offsets, token, weight, row = (perm["offsets"], perm["sorted_token"], perm["sorted_w"],
                                    perm["slot_to_row"])
     n = T * K

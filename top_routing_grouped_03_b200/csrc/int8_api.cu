@@ -504,7 +504,8 @@ int moe_quantize_rows(const moe_bf16* x, long long rows, int cols, int8_t* q, fl
 }
 
 size_t moe_int8_workspace_size(int T, int N, int K) {
-    return check_dense(T, N, K) == MOE_OK ? dense_layout(T, N, K).total : 0;
+    // a handful of tokens needs none
+    return check_dense(T, N, K) != MOE_OK || few_linear_ok(T, K) ? 0 : dense_layout(T, N, K).total;
 }
 
 int moe_int8_matmul(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
@@ -514,9 +515,6 @@ int moe_int8_matmul(const int8_t* xq, const float* x_scale, const int8_t* wq, co
     if (rc) return rc;
     if (!wq || !w_scale || (T > 0 && (!xq || !x_scale || !out))) return MOE_ERR_ARG;
     if (!aligned16(xq) || !aligned16(wq) || !aligned16(w_scale) || !aligned16(out)) return MOE_ERR_ALIGN;
-    const DenseLayout L = dense_layout(T, N, K);
-    if (!workspace || ws_bytes < L.total) return MOE_ERR_WORKSPACE;
-    if ((reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0) return MOE_ERR_ALIGN;
     if (T == 0) return MOE_OK;
     cudaStream_t s = as_stream(stream);
     if (few_linear_ok(T, K))
@@ -524,6 +522,9 @@ int moe_int8_matmul(const int8_t* xq, const float* x_scale, const int8_t* wq, co
                                  reinterpret_cast<bf16*>(out), num_sms_current(), s) == cudaSuccess
                    ? MOE_OK
                    : MOE_ERR_CUDA;
+    const DenseLayout L = dense_layout(T, N, K);
+    if (!workspace || ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0) return MOE_ERR_ALIGN;
     if (cudaMemsetAsync(workspace, 0, 4ull * L.clear_words, s) != cudaSuccess) return MOE_ERR_CUDA;
     return launch_dense(xq, x_scale, wq, w_scale, T, N, K, out, workspace, L, s, false) == cudaSuccess
                ? MOE_OK
@@ -536,9 +537,6 @@ int moe_int8_linear(const moe_bf16* x, const int8_t* wq, const float* w_scale, i
     if (rc) return rc;
     if (!wq || !w_scale || (T > 0 && (!x || !out))) return MOE_ERR_ARG;
     if (!aligned16(x) || !aligned16(wq) || !aligned16(w_scale) || !aligned16(out)) return MOE_ERR_ALIGN;
-    const DenseLayout L = dense_layout(T, N, K);
-    if (!workspace || ws_bytes < L.total) return MOE_ERR_WORKSPACE;
-    if ((reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0) return MOE_ERR_ALIGN;
     if (T == 0) return MOE_OK;
     cudaStream_t s = as_stream(stream);
     if (few_linear_ok(T, K))
@@ -546,6 +544,9 @@ int moe_int8_linear(const moe_bf16* x, const int8_t* wq, const float* w_scale, i
                                  K, reinterpret_cast<bf16*>(out), num_sms_current(), s) == cudaSuccess
                    ? MOE_OK
                    : MOE_ERR_CUDA;
+    const DenseLayout L = dense_layout(T, N, K);
+    if (!workspace || ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0) return MOE_ERR_ALIGN;
     QuantizeLaunch q{};
     q.x = x;
     q.rows = T;
