@@ -289,6 +289,8 @@ struct Int8FewExperts {
     const bf16* residual;  // or NULL
     int T, D, E, K, f;
     float* h;              // [T*K, f]
+    int8_t* hq;            // the same in 8 bits
+    float* hs;             // with a scale for each row [T*K]
     bf16* out;
 };
 bool few_experts_ok(int T, int D, int K, int f);

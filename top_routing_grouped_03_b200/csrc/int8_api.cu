@@ -225,8 +225,9 @@ cudaError_t run_combine(const ExpertsLayout& L, void* ws, Sum sum, const float* 
     return launch_combine(c, sms, s, true);
 }
 
-// The whole of moe_experts_int8 for a handful of rows: two launches.
-cudaError_t run_few(const moe_int8_experts& p, float* h, moe_bf16* out, int sms, cudaStream_t s) {
+// The whole of moe_experts_int8 for a handful of rows: three launches.
+cudaError_t run_few(const moe_int8_experts& p, const ExpertsLayout& L, void* ws, moe_bf16* out, int sms,
+                    cudaStream_t s) {
     Int8FewExperts a{};
     a.xq = p.xq;
     a.x_scale = p.x_scale;
@@ -239,7 +240,9 @@ cudaError_t run_few(const moe_int8_experts& p, float* h, moe_bf16* out, int sms,
     a.down_scale = p.down_scale;
     a.residual = reinterpret_cast<const bf16*>(p.residual);
     a.T = p.T; a.D = p.D; a.E = p.E; a.K = p.K; a.f = p.f;
-    a.h = h;
+    a.h = at<float>(ws, L.h);
+    a.hq = at<int8_t>(ws, L.hq);
+    a.hs = at<float>(ws, L.hs);
     a.out = reinterpret_cast<bf16*>(out);
     return launch_few_experts(a, sms, s);
 }
@@ -380,7 +383,7 @@ int layer_int8(const moe_layer_params* p, const RouteLogitsLaunch* rule, const m
     e.residual = p->residual;
     e.T = T; e.D = D; e.E = E; e.K = K; e.f = f;
     if (!shared && few_experts_ok(T, D, K, f))
-        return run_few(e, at<float>(ws, L.x.h), out, sms, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+        return run_few(e, L.x, ws, out, sms, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     const Sum sum = pick_sum(T, D, E, K, f, p->flags, sms);
     // the accumulator: the routed rows' reductions and the shared expert's
     float* acc = sum == Sum::kAccumulator || shared ? at<float>(ws, L.x.acc) : nullptr;
@@ -586,7 +589,7 @@ int moe_experts_int8(const moe_int8_experts* p, moe_bf16* out, void* workspace, 
     cudaStream_t s = as_stream(stream);
     const int sms = num_sms_current();
     if (few_experts_ok(T, D, K, f))
-        return run_few(*p, at<float>(workspace, L.h), out, sms, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+        return run_few(*p, L, workspace, out, sms, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     if (cudaMemsetAsync(workspace, 0, L.zero_end, s) != cudaSuccess) return MOE_ERR_CUDA;
     const Sum sum = pick_sum(T, D, E, K, f, p->flags, sms);
     float* acc = sum == Sum::kAccumulator ? at<float>(workspace, L.acc) : nullptr;

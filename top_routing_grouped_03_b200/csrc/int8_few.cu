@@ -9,10 +9,13 @@
 // tokens are looked at, so that quantising them (every CTA for itself: a few KB) hides
 // behind the weights' latency and costs no launch of its own.
 //   * linear: 4096 x 4096, one token: 12.9 + 2.3 us (tensor cores + row quantisation) before.
-//   * experts: one launch for gate_up (h in fp32) and one that quantises h, multiplies with the
-//     down weights and adds a token's experts in registers in row order: no accumulator, no
-//     atomics, no combine.  Each (token, expert) row reads its weights for itself; at most
-//     kFewRows rows, so two tokens with a common expert at worst read it twice.
+//   * experts: gate_up (h in fp32), the rows of h to 8 bits (quantize.cu), and down, which adds a
+//     token's experts in registers in row order: no accumulator, no atomics, no combine.  down
+//     starts with gate_up and brings its weights into L2 until h is there.  (h quantised by
+//     every CTA of down for itself, as linear does with its tokens, took 8 us longer than the
+//     launch in between: 512 CTAs read the same 32 KB.)  Each (token, expert) row reads its
+//     weights for itself; at most kFewRows rows, so two tokens with a common expert at worst
+//     read it twice.
 #include <algorithm>
 
 #include "quantize.cuh"
@@ -49,15 +52,14 @@ __device__ __forceinline__ float scaled(int sum, float col_scale, float row_scal
 // `rows` rows of `cols` values (a multiple of 16) as 8-bit integers to shared memory q (rows
 // `stride` bytes apart) and their scales to `scale`; all threads of the CTA, per: warps to a row
 // (a power of two).  part: one word per warp.
-template <typename T>
-__device__ __forceinline__ void quantise_rows(const T* x, int rows, int cols, int8_t* q, int stride,
+__device__ __forceinline__ void quantise_rows(const bf16* x, int rows, int cols, int8_t* q, int stride,
                                               float* scale, uint32_t* part, int per) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = warp & (per - 1), step = per * kChunkBytes;
     for (int r0 = 0; r0 < rows; r0 += kWarps / per) {
         const int r = r0 + warp / per;
         const int n = r < rows ? cols : 0;
-        const T* row = x + static_cast<size_t>(r) * cols;
+        const bf16* row = x + static_cast<size_t>(r) * cols;
         const int c0 = (sub * 32 + lane) * 16;
         float first[16];
         uint32_t m = 0;
@@ -254,8 +256,6 @@ template <int R, int C>
 __global__ void __launch_bounds__(kThreads, kExpertCtas) few_down_kernel(Int8FewExperts a) {
     extern __shared__ __align__(16) int8_t sm[];  // h as 8-bit integers [rows, f]
     __shared__ int s_expert[kFewRows], s_token[kFewRows];
-    __shared__ float s_scale[kFewRows];
-    __shared__ uint32_t s_part[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = read_rows(a, s_expert, s_token);  // (older than gate_up's launch)
     const int my_row = min(lane, kFewRows - 1);
@@ -280,10 +280,11 @@ __global__ void __launch_bounds__(kThreads, kExpertCtas) few_down_kernel(Int8Few
             }
         }
     };
-    grid_dep_wait();  // h
-    quantise_rows(a.h, rows, a.f, sm, a.f, s_scale, s_part, 1);
+    grid_dep_wait();  // the rows of h
+    for (int i = threadIdx.x * 16; i < rows * a.f; i += kThreads * 16)
+        *reinterpret_cast<uint4*>(sm + i) = __ldcg(reinterpret_cast<const uint4*>(a.hq + i));
+    const float row_factor = lane < rows ? __ldcg(a.hs + my_row) * a.sorted_w[my_row] : 0.f;
     __syncthreads();
-    const float row_factor = lane < rows ? s_scale[my_row] * a.sorted_w[my_row] : 0.f;
     for (int d = first; d < a.D; d += step) {
         const float cs = lane < rows ? __ldg(a.down_scale + my_scale + d) : 0.f;
         float y = 0.f;
@@ -354,8 +355,17 @@ cudaError_t launch_few_experts(const Int8FewExperts& a, int num_sms, cudaStream_
         count_launches(1);
         return err;
     };
-    const cudaError_t err = go(few_gate_up_kernel, rows * a.f, static_cast<size_t>(a.T) * a.D, false);
+    cudaError_t err = go(few_gate_up_kernel, rows * a.f, static_cast<size_t>(a.T) * a.D, false);
     if (err != cudaSuccess) return err;
+    QuantizeLaunch q{};
+    q.x = a.h;
+    q.is_f32 = true;
+    q.rows = rows;
+    q.cols = a.f;
+    q.q = a.hq;
+    q.scale = a.hs;
+    q.row_count = a.offsets + a.E;
+    if ((err = launch_quantize(q, s, true)) != cudaSuccess) return err;
     const size_t smem = static_cast<size_t>(rows) * a.f;
     return chunks == 1   ? go(few_down_kernel<8, 1>, a.D, smem, true)
            : chunks == 2 ? go(few_down_kernel<4, 2>, a.D, smem, true)

@@ -4,8 +4,8 @@
 // (rint: to nearest, ties to even), so that x ~ q scale and |q| <= 127.  The quotient of
 // 127 x and amax, correctly rounded to fp32, decides: for bf16 x both are exact and the
 // quotient is never rounded onto a tie, so q is the exact rounding of the real quotient.
-// Most elements take a product with 1 / amax instead, which is within 3e-5 of the quotient;
-// only one that lands within 6e-5 of a tie is divided.
+// Most elements take a product with 127 / amax instead, which is within 2.3e-5 of the
+// quotient; one that lands within 2.5e-5 of a tie is divided.
 //
 // Bound by memory: a row is read once (kept in registers between the maximum and the
 // rounding) and written once.  As many threads take a row as give each 16 columns, from a warp
@@ -24,8 +24,8 @@ constexpr int kChunk = 16;  // columns of one thread at a time: one 16-byte stor
 template <typename T, int kRowThreads, int kKeep>
 __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(QuantizeLaunch a) {
     __shared__ uint32_t s_max[kThreads / 32];
+    grid_dep_launch();  // what follows may start up to its own wait
     grid_dep_wait();
-    grid_dep_launch();
     const int lane = threadIdx.x % kRowThreads;
     if (a.clear && blockIdx.x == 0)
         for (int i = threadIdx.x; i < a.clear_words; i += kThreads) a.clear[i] = 0u;
