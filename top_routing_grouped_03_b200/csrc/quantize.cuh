@@ -19,14 +19,6 @@ __device__ __forceinline__ void load_chunk(const bf16* p, float (&v)[16]) {
         v[8 * h + 6] = bf16_lo(w.w); v[8 * h + 7] = bf16_hi(w.w);
     }
 }
-__device__ __forceinline__ void load_chunk(const float* p, float (&v)[16]) {
-    const float4* s = reinterpret_cast<const float4*>(p);
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-        const float4 w = __ldcg(s + h);
-        v[4 * h] = w.x; v[4 * h + 1] = w.y; v[4 * h + 2] = w.z; v[4 * h + 3] = w.w;
-    }
-}
 
 // max of |v| on the bit patterns: a NaN counts above infinity instead of being dropped
 __device__ __forceinline__ uint32_t abs_max(uint32_t m, const float (&v)[16]) {
@@ -55,28 +47,28 @@ __device__ __forceinline__ RowScale row_scale(uint32_t m) {
     return s;
 }
 
-// rint(127 v / amax) of 16 values to q.  v * factor is within 2.3e-5 of the quotient (three
-// roundings, 2^-24 each, of numbers up to 127); one that lands within 2.5e-5 of a tie is divided.
-// (As a call for all 16, to keep the code short, the rare path cost decode batches 4 us: a
-// warp takes it for 3% of its chunks.)  A row that is not finite is written as zeros.
-__device__ __forceinline__ void store_chunk(int8_t* q, const float (&v)[16], const RowScale& s) {
+// rint(127 v / amax) in the low byte of the result (two's complement).  v * factor is within 2.3e-5
+// of the quotient (three roundings, 2^-24 each, of numbers up to 127); one that lands within
+// 2.5e-5 of a tie is divided.  (A call for 16 values at a time, to keep the code short, cost decode
+// batches 4 us: a warp takes the rare path for 3% of its 512 values.)
+__device__ __forceinline__ uint32_t quantise(float v, const RowScale& s) {
     constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to the low bits
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if (s.scale == s.scale) {
-        uint32_t b[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float n = v[j] * s.pre, r = n * s.factor;
-            float m = r + kRound;
-            if (fabsf(r - (m - kRound)) > 0.5f - 2.5e-5f) m = __fdiv_rn(127.f * n, s.amax) + kRound;
-            b[j] = __float_as_uint(m);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w[j] = __byte_perm(__byte_perm(b[4 * j], b[4 * j + 1], 0x0040),
-                               __byte_perm(b[4 * j + 2], b[4 * j + 3], 0x0040), 0x5410);
-    }
-    *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+    const float n = v * s.pre, r = n * s.factor;
+    float m = r + kRound;
+    if (fabsf(r - (m - kRound)) > 0.5f - 2.5e-5f) m = __fdiv_rn(127.f * n, s.amax) + kRound;
+    return __float_as_uint(m);
+}
+
+// Four values as bytes; zeros in a row that is not finite.
+__device__ __forceinline__ uint32_t quantise4(const float* v, const RowScale& s) {
+    if (s.scale != s.scale) return 0u;
+    return __byte_perm(__byte_perm(quantise(v[0], s), quantise(v[1], s), 0x0040),
+                       __byte_perm(quantise(v[2], s), quantise(v[3], s), 0x0040), 0x5410);
+}
+
+__device__ __forceinline__ void store_chunk(int8_t* q, const float (&v)[16], const RowScale& s) {
+    *reinterpret_cast<uint4*>(q) =
+        make_uint4(quantise4(v, s), quantise4(v + 4, s), quantise4(v + 8, s), quantise4(v + 12, s));
 }
 
 }  // namespace
