@@ -80,7 +80,7 @@ __device__ __forceinline__ void quantise_rows(const bf16* x, int rows, int cols,
             for (int w = 0; w < per; ++w) m = max(m, part[(warp & ~(per - 1)) + w]);
         }
         const RowScale s = row_scale(m);
-        if (n > 0 && sub == 0 && lane == 0) scale[r] = s.scale;
+        if (n > 0 && sub == 0 && lane == 0) scale[r] = s.scale();
         if (c0 < n) store_chunk(q + r * stride + c0, first, s);
         for (int c = c0 + step; c < n; c += step) {
             float v[16];

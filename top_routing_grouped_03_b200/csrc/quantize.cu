@@ -4,8 +4,8 @@
 // (rint: to nearest, ties to even), so that x ~ q scale and |q| <= 127.  The quotient of
 // 127 x and amax, correctly rounded to fp32, decides: for bf16 x both are exact and the
 // quotient is never rounded onto a tie, so q is the exact rounding of the real quotient.
-// Most elements take a product with 127 / amax instead, which is within 2.3e-5 of the
-// quotient; one that lands within 2.5e-5 of a tie is divided.
+// Most elements take a product with 127 / amax instead, which is within 3.1e-5 of the
+// quotient; those within 3.5e-5 of a tie are divided.
 //
 // Bound by memory: a row is read once (kept in registers between the maximum and the
 // rounding) and written once.  As many threads take a row as give each 16 columns, from a warp
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(QuantizeLaunch 
     }
     if (cols == 0) return;
     const RowScale s = row_scale(m);
-    if (lane == 0) a.scale[row] = s.scale;
+    if (lane == 0) a.scale[row] = s.scale();
 #pragma unroll
     for (int k = 0; k < kKeep; ++k) store_share<kRowThreads, T>(q, k * kStep, cols, lane, keep[k], s);
     for (int c = kKeep * kStep; c < cols; c += kStep) {

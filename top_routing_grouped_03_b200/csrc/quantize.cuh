@@ -20,50 +20,71 @@ __device__ __forceinline__ void load_chunk(const bf16* p, float (&v)[16]) {
     }
 }
 
-// max of |v| on the bit patterns: a NaN counts above infinity instead of being dropped
-__device__ __forceinline__ uint32_t abs_max(uint32_t m, const float (&v)[16]) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-    return m;
+// max(m, |a|, |b|); a NaN stays
+__device__ __forceinline__ float max_nan3(float m, float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+    return r;
 }
 
-// A row's scale, amax after a multiplication by the power of two `pre`, and the factor
-// pre * 127 / amax.
+// The bits of max |v| (m: those of a maximum so far), which order like the numbers; a NaN counts
+// above infinity instead of being dropped.
+__device__ __forceinline__ uint32_t abs_max(uint32_t m, const float (&v)[16]) {
+    float f = __uint_as_float(m);
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) f = max_nan3(f, v[j], v[j + 1]);
+    return __float_as_uint(f);
+}
+
+// What rounds a row's values: `top` its abs_max, amax = top * pre with a power of two, and
+// pre * 127 / top.  The power of two brings extreme rows to where 127 v and 1 / amax are normal
+// numbers (what it pushes below the smallest one rounds to 0 anyway).
 struct RowScale {
-    float scale, pre, amax, factor;
+    float top, pre, amax, factor;
+    bool finite;
+
+    // the row's scale: NaN in a row with a NaN or an infinity.  (A division: for one thread of a
+    // row; by all of them it was a fifth of the kernel's instructions.)
+    __device__ __forceinline__ float scale() const {
+        return finite ? __fdiv_rn(top, 127.f) : __int_as_float(0x7fc00000);
+    }
 };
 
-// From the row's abs_max.  The power of two brings extreme rows to where 127 v and 1 / amax are
-// normal numbers (what it pushes below the smallest one rounds to 0 anyway).  A row with a
-// NaN or an infinity has scale NaN.
 __device__ __forceinline__ RowScale row_scale(uint32_t m) {
-    const float top = __uint_as_float(m);
-    const bool finite = m < 0x7f800000u;
     RowScale s;
-    s.pre = top > 0x1p100f ? 0x1p-64f : top < 0x1p-60f ? 0x1p64f : 1.f;
-    s.amax = top * s.pre;
-    s.factor = finite && top > 0.f ? 127.f * __frcp_rn(s.amax) : 0.f;
-    s.scale = finite ? __fdiv_rn(top, 127.f) : __int_as_float(0x7fc00000);
+    s.top = __uint_as_float(m);
+    s.finite = m < 0x7f800000u;
+    s.pre = s.top > 0x1p100f ? 0x1p-64f : s.top < 0x1p-60f ? 0x1p64f : 1.f;
+    s.amax = s.top * s.pre;
+    float inv;  // within 2^-23 of 1 / amax
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s.amax));
+    s.factor = s.finite && s.top > 0.f ? 127.f * inv : 0.f;
     return s;
 }
 
-// rint(127 v / amax) in the low byte of the result (two's complement).  v * factor is within 2.3e-5
-// of the quotient (three roundings, 2^-24 each, of numbers up to 127); one that lands within
-// 2.5e-5 of a tie is divided.  (A call for 16 values at a time, to keep the code short, cost decode
-// batches 4 us: a warp takes the rare path for 3% of its 512 values.)
-__device__ __forceinline__ uint32_t quantise(float v, const RowScale& s) {
-    constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to the low bits
-    const float n = v * s.pre, r = n * s.factor;
-    float m = r + kRound;
-    if (fabsf(r - (m - kRound)) > 0.5f - 2.5e-5f) m = __fdiv_rn(127.f * n, s.amax) + kRound;
-    return __float_as_uint(m);
-}
-
-// Four values as bytes; zeros in a row that is not finite.
+// rint(127 v / amax) of four values, as bytes; zeros in a row that is not finite.  v * factor is
+// within 3.1e-5 of the quotient (numbers up to 127 with 2^-23 from the reciprocal and 2^-24 from
+// each product); where one of the four lands within 3.5e-5 of a tie they are divided.  One test for four values instead of one
+// each, and one maximum for two: 20 -> 16 instructions a value, which bound the bf16 rows.
+// (A call for 16 values, to keep the code short, cost decode batches 4 us: a warp takes
+// the rare path for 3% of its 512 values.)
 __device__ __forceinline__ uint32_t quantise4(const float* v, const RowScale& s) {
-    if (s.scale != s.scale) return 0u;
-    return __byte_perm(__byte_perm(quantise(v[0], s), quantise(v[1], s), 0x0040),
-                       __byte_perm(quantise(v[2], s), quantise(v[3], s), 0x0040), 0x5410);
+    constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to the low bits
+    float n[4], m[4], off = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        n[j] = v[j] * s.pre;
+        const float r = n[j] * s.factor;
+        m[j] = r + kRound;
+        off = fmaxf(off, fabsf(r - (m[j] - kRound)));
+    }
+    if (off > 0.5f - 3.5e-5f) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m[j] = __fdiv_rn(127.f * n[j], s.amax) + kRound;
+    }
+    const uint32_t q = __byte_perm(__byte_perm(__float_as_uint(m[0]), __float_as_uint(m[1]), 0x0040),
+                                   __byte_perm(__float_as_uint(m[2]), __float_as_uint(m[3]), 0x0040), 0x5410);
+    return s.finite ? q : 0u;
 }
 
 __device__ __forceinline__ void store_chunk(int8_t* q, const float (&v)[16], const RowScale& s) {
