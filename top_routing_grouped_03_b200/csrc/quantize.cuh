@@ -56,18 +56,18 @@ __device__ __forceinline__ RowScale row_scale(uint32_t m) {
     s.finite = m < 0x7f800000u;
     s.pre = s.top > 0x1p100f ? 0x1p-64f : s.top < 0x1p-60f ? 0x1p64f : 1.f;
     s.amax = s.top * s.pre;
-    float inv;  // within 2^-23 of 1 / amax
+    float inv;  // within 2^-22 of 1 / amax (documented: 2^-23 where 1 / amax is 1/2 to 1)
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s.amax));
     s.factor = s.finite && s.top > 0.f ? 127.f * inv : 0.f;
     return s;
 }
 
 // rint(127 v / amax) of four values, as bytes; zeros in a row that is not finite.  v * factor is
-// within 3.1e-5 of the quotient (numbers up to 127 with 2^-23 from the reciprocal and 2^-24 from
-// each product); where one of the four lands within 3.5e-5 of a tie they are divided.  One test for four values instead of one
+// within 4.6e-5 of the quotient (numbers up to 127 with 2^-22 from the reciprocal and 2^-24 from
+// each product); where one of the four lands within 5e-5 of a tie they are divided.  One test for four values instead of one
 // each, and one maximum for two: 20 -> 16 instructions a value, which bound the bf16 rows.
 // (A call for 16 values, to keep the code short, cost decode batches 4 us: a warp takes
-// the rare path for 3% of its 512 values.)
+// the rare path for 5% of its chunks of 512 values.)
 __device__ __forceinline__ uint32_t quantise4(const float* v, const RowScale& s) {
     constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to the low bits
     float n[4], m[4], off = 0.f;
@@ -78,7 +78,7 @@ __device__ __forceinline__ uint32_t quantise4(const float* v, const RowScale& s)
         m[j] = r + kRound;
         off = fmaxf(off, fabsf(r - (m[j] - kRound)));
     }
-    if (off > 0.5f - 3.5e-5f) {
+    if (off > 0.5f - 5e-5f) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) m[j] = __fdiv_rn(127.f * n[j], s.amax) + kRound;
     }
