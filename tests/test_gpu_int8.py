@@ -59,7 +59,8 @@ def test_quantize_extreme_rows(moe):
 
 
 SHAPES = [(1, 8, 16), (1, 4096, 4096), (3, 520, 1040), (8, 256, 2048), (9, 264, 2064), (77, 4104, 2064),
-          (127, 128, 128), (128, 256, 256), (129, 1032, 400), (300, 264, 144), (513, 776, 1024)]
+          (127, 128, 128), (128, 256, 256), (129, 1032, 400), (300, 264, 144), (513, 776, 1024),
+          (16, 1032, 8208), (40, 4096, 8192), (130, 264, 4112)]
 
 
 @pytest.mark.parametrize("T,N,K", SHAPES)

@@ -214,8 +214,11 @@ cudaError_t launch_int8_gemm(const Int8GemmLaunch& a, int num_sms, cudaStream_t 
                             ? (a.acc_out != nullptr && a.y_out == nullptr && a.y16_out == nullptr)
                             : (a.part != nullptr && a.tickets != nullptr && a.ticket_cap > 0));
     // A dense product's slices cost a round trip of partial sums; they pay where few tiles have a
-    // long K (100 x 512 x 8192: 21 against 26 us; 77 x 4104 x 2064 the other way: 15 against 11).
-    const bool worth = !dense || (4ll * ceil_div(a.rows, kTmRows) * p.nf <= num_sms && p.nk >= 32);
+    // long K (100 x 512 x 8192: 21 against 26 us; 77 x 4104 x 2064 the other way: 15 against 11),
+    // and for up to half as many tiles as SMs where it is twice as long (16 x 4096 x 8192: 18.5
+    // against 24.6 us; 128 x 4096 x 4096 the other way: 19.6 against 16.4).
+    const long long tiles = static_cast<long long>(ceil_div(a.rows, kTmRows)) * p.nf;
+    const bool worth = !dense || (4 * tiles <= num_sms && p.nk >= 32) || (2 * tiles <= num_sms && p.nk >= 64);
     p.ksplit_max = split && worth ? std::min(a.ksplit_max, kSplitSlicesMax) : 1;
     p.part = reinterpret_cast<float*>(a.part);
     p.part_rows = a.rows;
