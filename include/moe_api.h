@@ -483,6 +483,10 @@ MOE_API int moe_int8_linear(const moe_bf16* x, const int8_t* wq, const float* w_
  *   out[t, :] = bf16( residual[t, :] + sum over t's rows of sorted_w[r] * W_down^e h_r )
  * with W^e = scale[n] * wq[n, :] for weight row n.  Rows from expert_offsets[E] on are left
  * out (a capacity dropped them); a token without rows gets its residual (or 0).
+ * Sums are held in fp32, with one exception: without MOE_FLAG_DETERMINISTIC and with many rows an
+ * expert (128 on average), a row's products pass through 16-bit integers with one fp32 scale for
+ * each 32 columns, an error of up to 2^-16 of the largest of the 32 (the bf16 result rounds by up
+ * to 2^-8 of itself).  NaN and infinite scales or products show in their own columns either way.
  * No kernel waits for another CTA's work, so calls with workspaces of their own may run on
  * several streams at once.
  */

@@ -19,6 +19,13 @@ __device__ __forceinline__ void set_status(int* status, int code) {
     if (status != nullptr) atomicCAS(status, 0, code);
 }
 
+// max(m, |a|, |b|); a NaN stays
+__device__ __forceinline__ float max_nan3(float m, float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+    return r;
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t packed) {
     return __uint_as_float(packed << 16);
 }
@@ -304,12 +311,16 @@ cudaError_t launch_ep_recv_layout(const int32_t* recv_counts, int G, int El, int
 cudaError_t launch_ep_return_rows(const float* y, const int32_t* recv_row, int n, int D,
                                   float* y_ret, int num_sms, cudaStream_t s);
 
+// Rows as 16-bit integers: numbers are -kRows16Max to kRows16Max times their block's scale.  Below
+// them, so that a minimum finds them: -infinity, infinity and NaN.
+constexpr int kRows16Max = 32765, kRows16MinusInf = -32766, kRows16Inf = -32767, kRows16Nan = -32768;
+
 struct CombineLaunch {
     const bf16* residual;  // [T, D] added before the bf16 rounding, or NULL
     const float* out_acc;
     const float* y_sorted;
-    const int16_t* y16q_sorted;  // [T*K, D] already weighted rows as 16-bit integers with a scale for
-    const float* y16q_scale;     // each 32 columns [T*K, D / 32] (instead of y_sorted), or NULL
+    const int16_t* y16q_sorted;  // [T*K, D] already weighted rows as 16-bit integers (kRows16Max) with a
+    const float* y16q_scale;     // scale for each 32 columns [T*K, D / 32] (instead of y_sorted), or NULL
     const bf16* y16_sorted;  // [T*K, D] bf16 rows already weighted (instead of y_sorted), or NULL
     const int32_t* slot_to_row;
     const float* topk_w;

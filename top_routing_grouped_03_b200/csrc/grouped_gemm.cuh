@@ -961,48 +961,104 @@ __device__ __forceinline__ void i8_dense_epilogue(const Params& p, uint32_t tcol
 }
 
 // down rows for a sum over a token's experts by a later kernel: blocks of 32 columns of the
-// products as 16-bit integers with the scale max |product| / 32767 (times the row's factor w).
+// products as 16-bit integers with the scale max |product| / kRows16Max (times the row's factor w).
 // Nearly as few bytes as bf16 rows, but an error of 2^-16 of the block's largest value instead of
 // 2^-9 of each: bf16 rows would add as much again to the error of the bf16 result.  fp32
 // reductions into the tokens' rows (1 GB of them at 65536 x 4096) kept the tensor cores
 // waiting: 454 us.
 constexpr int kRows16Block = 32;
+
+// The 16-bit integers (fp32 bits of them added to 1.5 * 2^23, which rounds to the low bits) of a
+// block's products t for inv = kRows16Max / top.
+__device__ __forceinline__ void rows16_pack(const uint32_t (&t)[32], float inv, uint4 (&o)[4]) {
+    constexpr float kMagic = 12582912.f;
+    auto two = [&](int j) {
+        return __byte_perm(__float_as_uint(fmaf(__uint_as_float(t[j]), inv, kMagic)),
+                           __float_as_uint(fmaf(__uint_as_float(t[j + 1]), inv, kMagic)), 0x5410);
+    };
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        o[k] = make_uint4(two(8 * k), two(8 * k + 2), two(8 * k + 4), two(8 * k + 6));
+}
+__device__ __forceinline__ bool rows16_plain(float top) { return top > 0x1p-60f && top < 0x1p60f; }
+
+// A block whose largest magnitude `top` is infinite, a NaN, or too small or large for rows16_pack:
+// brings its finite values to ordinary sizes by a power of two, sets the others to what becomes
+// their integers, and `top` to the largest finite one.  Returns what the block's scale is to be
+// multiplied by.  A channel scale that is no number brings one block of every row here: its column
+// alone shows it (finite values below 2^-76 beside it become 0).
+__device__ __forceinline__ float rows16_rare(uint32_t (&t)[32], float& top) {
+    float finite = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const float a = fabsf(__uint_as_float(t[j]));
+        if (a < INFINITY) finite = fmaxf(finite, a);
+    }
+    const bool all = top < INFINITY;
+    const float pre = finite > 0x1p60f ? 0x1p-64f : all && finite < 0x1p-60f ? 0x1p64f : 1.f;
+    top = finite * pre;
+    if (!all) top = fmaxf(top, 0x1p-60f);  // (the scale must not be 0)
+    const float step = top * (1.f / kRows16Max);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const float v = __uint_as_float(t[j]);
+        const int code = isnan(v) ? kRows16Nan : v > 0.f ? kRows16Inf : kRows16MinusInf;
+        t[j] = __float_as_uint(isfinite(v) ? v * pre : code * step);
+    }
+    return 1.f / pre;
+}
+
 __device__ __forceinline__ void i8_rows16_epilogue(const Params& p, uint32_t tcol, int row0, int n,
                                                    float w, int col0, const float* scales, float* stage,
                                                    int lane) {
-    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to the low bits
     int16_t* y0 = p.y16q_out + static_cast<size_t>(row0) * p.out_cols + col0;
-    float block_scale[4];
-    uint32_t v[2][32];  // a block in work, the next one on its way from tensor memory
-    tmem_ld32(tcol, v[0]);
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        uint32_t(&t)[32] = v[b & 1];
-        tmem_ld_wait_dep(t);
-        if (b + 1 < 4) tmem_ld32(tcol + (b + 1) * kRows16Block, v[(b + 1) & 1]);
-        scale_columns<32>(t, scales + b * kRows16Block);
+    float* s0 = p.y16q_scale + static_cast<size_t>(row0 + lane) * (p.out_cols / kRows16Block) +
+                col0 / kRows16Block;
+    const size_t stride = sizeof(int16_t) * p.out_cols;
+    auto largest = [](const uint32_t(&t)[32]) {
         float top = 0.f;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) top = fmaxf(top, fabsf(__uint_as_float(t[j])));
-        const bool any = top > 1e-30f && top < INFINITY;
-        const float inv = any ? __fdividef(32767.f, top) : 0.f;
-        // (a NaN comes in by w; products that overflow make their block NaN)
-        block_scale[b] = any ? w * (top * (1.f / 32767.f)) : w * (top < 1.f ? 0.f : NAN);
-        auto two = [&](int j) {
-            return __byte_perm(__float_as_uint(fmaf(__uint_as_float(t[j]), inv, kMagic)),
-                               __float_as_uint(fmaf(__uint_as_float(t[j + 1]), inv, kMagic)), 0x5410);
-        };
-        uint4 o[4];
+        for (int j = 0; j < 32; j += 2) top = max_nan3(top, __uint_as_float(t[j]), __uint_as_float(t[j + 1]));
+        return top;
+    };
+    float block_scale[4];
+    bool rare = false;
+    uint4 o[4];
+    {
+        uint32_t v[2][32];  // a block in work, the next one on its way from tensor memory
+        tmem_ld32(tcol, v[0]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            o[k] = make_uint4(two(8 * k), two(8 * k + 2), two(8 * k + 4), two(8 * k + 6));
-        store_rows64(o, y0 + b * kRows16Block, sizeof(int16_t) * p.out_cols, n, stage, lane);
+        for (int b = 0; b < 4; ++b) {
+            uint32_t(&t)[32] = v[b & 1];
+            tmem_ld_wait_dep(t);
+            if (b + 1 < 4) tmem_ld32(tcol + (b + 1) * kRows16Block, v[(b + 1) & 1]);
+            scale_columns<32>(t, scales + b * kRows16Block);
+            const float top = largest(t);
+            const bool plain = rows16_plain(top);
+            rare |= !plain && top != 0.f;
+            rows16_pack(t, plain ? __fdividef(static_cast<float>(kRows16Max), top) : 0.f, o);
+            // (0 products: scale 0; a row that is no number comes in by w)
+            block_scale[b] = w * (plain ? top * (1.f / kRows16Max) : 0.f);
+            store_rows64(o, y0 + b * kRows16Block, stride, n, stage, lane);
+        }
     }
-    if (lane < n)
-        *reinterpret_cast<float4*>(p.y16q_scale +
-                                   static_cast<size_t>(row0 + lane) * (p.out_cols / kRows16Block) +
-                                   col0 / kRows16Block) =
-            make_float4(block_scale[0], block_scale[1], block_scale[2], block_scale[3]);
+    if (lane < n) *reinterpret_cast<float4*>(s0) = make_float4(block_scale[0], block_scale[1],
+                                                               block_scale[2], block_scale[3]);
+    if (!__any_sync(0xffffffffu, rare)) return;
+    // (again from tensor memory, one copy of the code for the four blocks: as a branch of the loop
+    // above it cost a kernel that never takes it 3%, 297 -> 307 us)
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b) {
+        uint32_t t[32];
+        tmem_ld32(tcol + b * kRows16Block, t);
+        tmem_ld_wait_dep(t);
+        scale_columns<32>(t, scales + b * kRows16Block);
+        float top = largest(t), post = 1.f;
+        if (!rows16_plain(top) && top != 0.f) post = rows16_rare(t, top);
+        rows16_pack(t, top > 0.f ? __fdividef(static_cast<float>(kRows16Max), top) : 0.f, o);
+        if (lane < n) s0[b] = w * (top * (1.f / kRows16Max)) * post;
+        store_rows64(o, y0 + b * kRows16Block, stride, n, stage, lane);
+    }
 }
 
 __device__ __forceinline__ int4 add4(int4 a, int4 b) {

@@ -20,13 +20,6 @@ __device__ __forceinline__ void load_chunk(const bf16* p, float (&v)[16]) {
     }
 }
 
-// max(m, |a|, |b|); a NaN stays
-__device__ __forceinline__ float max_nan3(float m, float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
-    return r;
-}
-
 // The bits of max |v| (m: those of a maximum so far), which order like the numbers; a NaN counts
 // above infinity instead of being dropped.
 __device__ __forceinline__ uint32_t abs_max(uint32_t m, const float (&v)[16]) {
