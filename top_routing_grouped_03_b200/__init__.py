@@ -55,6 +55,8 @@ class RouteRule(ctypes.Structure):
         ("n_group", ctypes.c_int), ("topk_group", ctypes.c_int), ("group_top", ctypes.c_int),
         ("renorm", ctypes.c_int), ("scale", ctypes.c_float),
     ]
+    # set by route_rule(): the bias that select_bias points to, its CUDA device and its length
+    keep = device = E = None
 
 
 class Int8Experts(ctypes.Structure):
@@ -209,6 +211,7 @@ def route(x, w_router, K, logit_bias=None, w_shared_gate=None, workspace=None, s
     T, D = x.shape
     E = w_router.shape[0]
     dev = x.device
+    _check_rule(rule, E, x)
     ws = workspace if workspace is not None else alloc_workspace(T, D, E, K, 128, 0, dev)
     idx = torch.empty((T, K), dtype=torch.int32, device=dev)
     w = torch.empty((T, K), dtype=torch.float32, device=dev)
@@ -344,16 +347,29 @@ def _q(t, dtype, index):
 
 def route_rule(E, K, score="softmax", select_bias=None, n_group=1, topk_group=1, group_top=None,
                renorm=True, scale=1.0) -> RouteRule:
-    """A moe_route_rule.  group_top defaults to 2 with a select_bias (a group is judged by its two
+    """A moe_route_rule for routers of E experts (and K of them a token, which the groups that
+    stay have to hold).  group_top defaults to 2 with a select_bias (a group is judged by its two
     best keys) and 1 without."""
     if select_bias is not None:
         _need(select_bias.shape == (E,), "route_rule (select_bias must be [E])")
+    if n_group > 0 and E % n_group == 0:
+        _need(K <= topk_group * (E // n_group), "route_rule (K experts in the groups that stay)")
     if group_top is None:
         group_top = 1 if select_bias is None else 2
-    bias = None if select_bias is None else _q(select_bias, F32, select_bias.get_device())
-    rule = RouteRule(SCORES[score], bias, n_group, topk_group, group_top, 1 if renorm else 0, scale)
-    rule.keep = select_bias  # the rule holds a bare pointer to it
+    rule = RouteRule(SCORES[score], _p(select_bias, F32), n_group, topk_group, group_top,
+                     1 if renorm else 0, scale)
+    rule.keep, rule.E = select_bias, E
+    rule.device = None if select_bias is None else select_bias.get_device()
     return rule
+
+
+def _check_rule(rule, E, on):
+    """A rule's bias is as long as the router has experts, and on the device of tensor ``on``."""
+    if rule is None:
+        return
+    _need(rule.E is None or rule.E == E, f"route_rule (made for {rule.E} experts, used with {E})")
+    if rule.device is not None and rule.device != on.get_device():
+        raise ValueError(f"route_rule: select_bias on cuda:{rule.device}, tensors on {on.device}")
 
 
 @_on_device_of
@@ -566,6 +582,7 @@ class MoELayer:
         self.select_bias = select_bias
         self.capacity_factor = float(capacity_factor)
         self.min_capacity = int(min_capacity)
+        _check_rule(rule, self.E, w_router)
         self.rule = rule  # a route_rule(...) instead of score / select_bias / bf16_weights
         self._int8 = None
         self._ws = None
@@ -604,6 +621,7 @@ class MoELayer:
         T = x.shape[0]
         if x.shape[1] != self.D:
             raise MoEError(-1, "moe_layer_forward (x has the wrong width)")
+        _check_rule(self.rule, self.E, x)
         out = out if out is not None else torch.empty((T, self.D), dtype=torch.bfloat16,
                                                       device=x.device)
         ws = self.workspace(T)
