@@ -76,16 +76,22 @@ __device__ __forceinline__ float quick_reciprocal(float v) {
     return r;
 }
 
-// What two fp32 keys have to differ by for their order to be certain (twice this for scores
-// of groups, sums of two keys).  With a bias, per key: a sigmoid is off by at most 5e-7 (its
-// exponential's relative error counts s (1 - s) <= 1/4 times, and |r| s (1 - s) <= 0.23; a
-// reciprocal by 2 ulp), a softmax by 3e-6 (the same exponential and a sum of 512 terms), the sum
-// with the bias by 2^-24 of its size.  Without a bias only softmax sums are compared; their
-// common denominator does not matter, and a term is off by (|r - max| + 4) 2^-23 of its
-// size: 1.5e-5 for logits down to 100 below the largest, and what is smaller is 0.
+// What two fp32 keys (size: of the larger) have to differ by for their order to be certain, with a
+// bias: a sigmoid is off by at most 5e-7 (its exponential's relative error counts
+// s (1 - s) <= 1/4 times, and |r| s (1 - s) <= 0.23; a reciprocal by 2 ulp), a softmax by 3e-6 (the
+// same exponential and a sum of 512 terms), the sum with the bias by 2^-24 of its size.
 __device__ __forceinline__ float uncertain(const RouteLogitsLaunch& a, float size) {
-    if (a.select_bias == nullptr) return 1.5e-5f * fabsf(size);
     return (a.score_mode == 0 ? 6e-6f : 1.3e-6f) + 2.5e-7f * fabsf(size);
+}
+
+// How far what a group is judged by may be off, size: the sum of its (at most two) keys'
+// magnitudes; their own sum may be far smaller, with biases of either sign, and its error is not.
+// With a bias as two keys differ above (2^-24 of size for the keys and as much for the sum).  Without
+// one only sums of scores are not exact (their common denominator does not matter): a term is off by
+// (|r - max| + 4) 2^-23 of its size, 1.5e-5 for logits down to 100 below the largest, and where it
+// is below the smallest normal number, by that.
+__device__ __forceinline__ float group_error(const RouteLogitsLaunch& a, float size) {
+    return a.select_bias ? uncertain(a, size) : 1.5e-5f * size + 2.5e-38f;
 }
 
 template <typename V>
@@ -239,17 +245,25 @@ __device__ __forceinline__ int count_larger(const uint64_t* buf, int n, uint64_t
     return rank;
 }
 
-// The value that a group is judged by, from its two best keys (0: none).
-__device__ __forceinline__ uint32_t judged(const RouteLogitsLaunch& a, uint32_t m1, uint32_t m2) {
-    if (a.group_top == 1) return m1;
-    return ordered(group_score(unordered(m1), m2 ? unordered(m2) : -INFINITY, 2));
+// What a group is judged by, from its two best keys (0: none), and the sum of their magnitudes (0
+// where the best one is infinite: nothing is uncertain then).
+struct Judged {
+    uint32_t value;
+    float size;
+};
+__device__ __forceinline__ Judged judged(const RouteLogitsLaunch& a, uint32_t m1, uint32_t m2) {
+    const float k1 = unordered(m1), k2 = m2 ? unordered(m2) : -INFINITY;
+    const bool finite = fabsf(k1) < INFINITY;
+    if (a.group_top == 1) return {m1, finite ? fabsf(k1) : 0.f};
+    return {ordered(group_score(k1, k2, 2)),
+            finite ? fabsf(k1) + (k2 > -INFINITY ? fabsf(k2) : 0.f) : 0.f};
 }
 
 // Groups of 32 experts are one register of the warp each: lane g gets what group g is judged by,
 // from one or two warp-wide maxima a group.
 template <int NV>
-__device__ __forceinline__ uint32_t groups_in_registers(const RouteLogitsLaunch& a,
-                                                        const uint32_t (&key)[NV], int lane) {
+__device__ __forceinline__ Judged groups_in_registers(const RouteLogitsLaunch& a,
+                                                      const uint32_t (&key)[NV], int lane) {
     uint32_t m1 = 0u, m2 = 0u;
 #pragma unroll
     for (int g = 0; g < NV; ++g) {
@@ -270,8 +284,7 @@ __device__ __forceinline__ uint32_t groups_in_registers(const RouteLogitsLaunch&
 
 // The same for groups of any size, whose keys are in sm, each group padded: group_lpg lanes (a
 // power of two) look through a group, and all of them get its value.
-__device__ __forceinline__ uint32_t groups_in_memory(const RouteLogitsLaunch& a, const uint32_t* sm,
-                                                     int lane) {
+__device__ __forceinline__ Judged groups_in_memory(const RouteLogitsLaunch& a, const uint32_t* sm, int lane) {
     const int S = a.group_size, lpg = a.group_lpg;
     const int g = lane >> a.group_shift, sub = lane & (lpg - 1);
     uint32_t m1 = 0u, m2 = 0u;
@@ -287,13 +300,13 @@ __device__ __forceinline__ uint32_t groups_in_memory(const RouteLogitsLaunch& a,
     return judged(a, m1, m2);
 }
 
-// The groups that stay (a bit each): gs is what group g is judged by, in the lanes that speak for
+// The groups that stay (a bit each): j is what group g is judged by, in the lanes that speak for
 // one.  *near: the groups on either side of the border whose scores are not certain to be on
 // theirs (0: none).
-__device__ __forceinline__ unsigned pick_groups(const RouteLogitsLaunch& a, uint32_t gs, int g, bool speaks,
+__device__ __forceinline__ unsigned pick_groups(const RouteLogitsLaunch& a, Judged j, int g, bool speaks,
                                                 bool exact, unsigned* near, int lane) {
     unsigned allowed = 0;
-    uint32_t left = speaks ? gs : 0u;
+    uint32_t left = speaks ? j.value : 0u;
     for (int i = 0; i < a.topk_group; ++i) {
         // the best one left; equal ones: the lowest lane, which speaks for the lowest group
         const unsigned who = __ballot_sync(kAll, left == __reduce_max_sync(kAll, left));
@@ -304,15 +317,15 @@ __device__ __forceinline__ unsigned pick_groups(const RouteLogitsLaunch& a, uint
     const bool stays = speaks && left == 0u;
     *near = 0;
     if (!exact) {
-        const float last = unordered(__reduce_min_sync(kAll, stays ? gs : 0xffffffffu));
-        const float after = unordered(__reduce_max_sync(kAll, speaks && !stays ? gs : 0u));
-        const float tol = 2.f * uncertain(a, last);
-        if (after > -INFINITY && !(last - after > tol)) {
-            const float v = unordered(gs);
+        // the score lies between lo and hi
+        const float v = unordered(j.value), err = group_error(a, j.size);
+        const bool known = err < INFINITY;
+        const float lo = known ? v - err : -INFINITY, hi = known ? v + err : INFINITY;
+        const float last = unordered(__reduce_min_sync(kAll, stays ? ordered(lo) : 0xffffffffu));
+        const float after = unordered(__reduce_max_sync(kAll, speaks && !stays ? ordered(hi) : 0u));
+        if (after > -INFINITY && !(last > after))
             *near = __reduce_or_sync(
-                kAll, speaks && (stays ? !(v - after > tol) : v > -INFINITY && !(last - v > tol)) ? 1u << g
-                                                                                                 : 0u);
-        }
+                kAll, speaks && (stays ? !(lo > after) : hi > -INFINITY && !(last > hi)) ? 1u << g : 0u);
     }
     return allowed;
 }
@@ -385,7 +398,7 @@ __device__ __forceinline__ void route_token(const RouteLogitsLaunch& a, long lon
     }
     unsigned allowed = kAll;
     if (grouped) {
-        uint32_t gs;
+        Judged gs;
         int g = lane;
         bool speaks = lane < a.n_group;
         if (a.whole_registers) {
