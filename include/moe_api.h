@@ -461,7 +461,8 @@ MOE_API int moe_quantize_rows(const moe_bf16* x, long long rows, int cols, int8_
  * multiple of 8 up to 2^20.  w_scale 16-byte aligned like the matrices.
  * workspace: moe_int8_workspace_size(T, N, K) bytes, 256-byte aligned; no initialisation.  A
  * handful of tokens (T <= 8 with T * K <= 65536) needs none: the size is 0 (as it is for
- * unsupported sizes) and workspace may be NULL.
+ * unsupported sizes) and workspace may be NULL: such a call neither reads nor writes one, its status
+ * word included (it has no device-side error to report).
  */
 MOE_API size_t moe_int8_workspace_size(int T, int N, int K);
 MOE_API int moe_int8_matmul(const int8_t* xq, const float* x_scale, const int8_t* wq,

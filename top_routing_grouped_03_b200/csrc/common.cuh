@@ -298,6 +298,7 @@ struct Int8FewExperts {
     float* h;              // [T*K, f]
     int8_t* hq;            // the same in 8 bits
     float* hs;             // with a scale for each row [T*K]
+    int* status;           // cleared (no kernel here has an error to report), or NULL
     bf16* out;
 };
 bool few_experts_ok(int T, int D, int K, int f);

@@ -225,9 +225,10 @@ cudaError_t run_combine(const ExpertsLayout& L, void* ws, Sum sum, const float* 
     return launch_combine(c, sms, s, true);
 }
 
-// The whole of moe_experts_int8 for a handful of rows: three launches.
-cudaError_t run_few(const moe_int8_experts& p, const ExpertsLayout& L, void* ws, moe_bf16* out, int sms,
-                    cudaStream_t s) {
+// The whole of moe_experts_int8 for a handful of rows: three launches.  status: the status word to
+// clear, NULL in a layer call (which has cleared it, and whose permutation may have set it).
+cudaError_t run_few(const moe_int8_experts& p, const ExpertsLayout& L, void* ws, int* status, moe_bf16* out,
+                    int sms, cudaStream_t s) {
     Int8FewExperts a{};
     a.xq = p.xq;
     a.x_scale = p.x_scale;
@@ -243,6 +244,7 @@ cudaError_t run_few(const moe_int8_experts& p, const ExpertsLayout& L, void* ws,
     a.h = at<float>(ws, L.h);
     a.hq = at<int8_t>(ws, L.hq);
     a.hs = at<float>(ws, L.hs);
+    a.status = status;
     a.out = reinterpret_cast<bf16*>(out);
     return launch_few_experts(a, sms, s);
 }
@@ -383,7 +385,7 @@ int layer_int8(const moe_layer_params* p, const RouteLogitsLaunch* rule, const m
     e.residual = p->residual;
     e.T = T; e.D = D; e.E = E; e.K = K; e.f = f;
     if (!shared && few_experts_ok(T, D, K, f))
-        return run_few(e, L.x, ws, out, sms, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+        return run_few(e, L.x, ws, nullptr, out, sms, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     const Sum sum = pick_sum(T, D, E, K, f, p->flags, sms);
     // the accumulator: the routed rows' reductions and the shared expert's
     float* acc = sum == Sum::kAccumulator || shared ? at<float>(ws, L.x.acc) : nullptr;
@@ -472,6 +474,7 @@ int moe_route_rule_ex(const moe_bf16* x, const moe_bf16* w_router, const float* 
     if (T == 0)
         return cudaMemsetAsync(expert_counts, 0, sizeof(int32_t) * E, s) == cudaSuccess ? MOE_OK
                                                                                         : MOE_ERR_CUDA;
+    if (cudaMemsetAsync(workspace, 0, kAlign, s) != cudaSuccess) return MOE_ERR_CUDA;  // the status word
     RouterLaunch a{};
     a.x = reinterpret_cast<const bf16*>(x);
     a.w_router = reinterpret_cast<const bf16*>(w_router);
@@ -589,7 +592,8 @@ int moe_experts_int8(const moe_int8_experts* p, moe_bf16* out, void* workspace, 
     cudaStream_t s = as_stream(stream);
     const int sms = num_sms_current();
     if (few_experts_ok(T, D, K, f))
-        return run_few(*p, L, workspace, out, sms, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+        return run_few(*p, L, workspace, at<int>(workspace, L.status), out, sms, s) == cudaSuccess ? MOE_OK
+                                                                                                   : MOE_ERR_CUDA;
     if (cudaMemsetAsync(workspace, 0, L.zero_end, s) != cudaSuccess) return MOE_ERR_CUDA;
     const Sum sum = pick_sum(T, D, E, K, f, p->flags, sms);
     float* acc = sum == Sum::kAccumulator ? at<float>(workspace, L.acc) : nullptr;

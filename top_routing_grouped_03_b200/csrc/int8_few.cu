@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, kExpertCtas) few_gate_up_kernel(Int8
     __shared__ int s_expert[kFewRows], s_token[kFewRows];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_dep_launch();  // down may start on its weights
+    if (a.status && blockIdx.x == 0 && threadIdx.x == 0) *a.status = MOE_OK;
     for (int i = threadIdx.x * 16; i < a.T * a.D; i += kThreads * 16)
         *reinterpret_cast<uint4*>(sm + i) = __ldg(reinterpret_cast<const uint4*>(a.xq + i));
     const int rows = read_rows(a, s_expert, s_token);
