@@ -542,6 +542,10 @@ MOE_API int moe_layer_forward_ex(const moe_layer_params* p, const moe_route_rule
                                  const moe_int8_weights* weights, moe_bf16* out, void* workspace,
                                  size_t ws_bytes, void* stream);
 
+/* moe_layer_plan for moe_layer_forward_ex with bf16 weights and this rule (or NULL). */
+MOE_API int moe_layer_plan_ex(const moe_layer_params* p, const moe_route_rule* rule, unsigned* step_mask,
+                              int* launches);
+
 #ifdef __cplusplus
 }
 #endif

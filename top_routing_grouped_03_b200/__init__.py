@@ -150,6 +150,8 @@ def lib() -> ctypes.CDLL:
         L.moe_layer_forward_ex.argtypes = [ctypes.POINTER(LayerParams), RP,
                                            ctypes.POINTER(Int8Weights), P, P, Z, P]
         L.moe_layer_forward_ex.restype = I
+        L.moe_layer_plan_ex.argtypes = [ctypes.POINTER(LayerParams), RP, P, P]
+        L.moe_layer_plan_ex.restype = I
         _lib = L
     return _lib
 
@@ -636,14 +638,15 @@ class MoELayer:
         return out
 
     def plan(self, T: int):
-        """(steps that launch kernels, kernels per call) for T tokens, from moe_layer_plan:
+        """(steps that launch kernels, kernels per call) for T tokens, from moe_layer_plan_ex:
         the step names of STEP_EVENT_NAMES whose interval holds work of their own."""
         x = torch.empty((0, self.D), dtype=BF16, device=self.w_router.device)
         prm = self.params(x)
         prm.T = T
         mask, n = ctypes.c_uint(0), ctypes.c_int(0)
-        _check(lib().moe_layer_plan(ctypes.byref(prm), ctypes.byref(mask), ctypes.byref(n)),
-               "moe_layer_plan")
+        _check_rule(self.rule, self.E, x)
+        _check(lib().moe_layer_plan_ex(ctypes.byref(prm), self.rule, ctypes.byref(mask), ctypes.byref(n)),
+               "moe_layer_plan_ex")
         steps = [name for i, name in enumerate(STEP_EVENT_NAMES) if mask.value >> i & 1]
         return steps, n.value
 

@@ -168,6 +168,9 @@ cudaError_t launch_route_logits(const RouteLogitsLaunch& a, int num_sms, cudaStr
 // moe_layer_forward with the routing of `rule` (NULL: of p).
 int layer_forward(const moe_layer_params* p, const RouteLogitsLaunch* rule, moe_bf16* out,
                   void* workspace, size_t ws_bytes, void* stream);
+// moe_layer_plan likewise.
+int layer_plan(const moe_layer_params* p, const RouteLogitsLaunch* rule, unsigned* step_mask,
+               int* launches);
 
 struct GroupedGemmLaunch {
     bool gate_up;               // true: SiLU(gate)*up epilogue -> h; false: down epilogue

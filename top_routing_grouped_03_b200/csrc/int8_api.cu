@@ -42,6 +42,14 @@ RouteLogitsLaunch rule_launch(const moe_route_rule* r) {
     return a;
 }
 
+// A rule in the place of p's own routing.
+int check_layer_rule(const moe_layer_params* p, const moe_route_rule* rule) {
+    int rc = check_shape(p->T, p->D, p->E, p->K, p->f, p->f_s);
+    if (rc) return rc;
+    if ((rc = check_rule(rule, p->E, p->K))) return rc;
+    return p->score_mode || p->select_bias || (p->flags & MOE_FLAG_BF16_WEIGHTS) ? MOE_ERR_ARG : MOE_OK;
+}
+
 // ---------------------------------------------------------------- dense product
 
 // The K steps of a tile may be cut into slices when the tiles cannot fill the GPU; the slices'
@@ -615,16 +623,22 @@ int moe_layer_forward_ex(const moe_layer_params* p, const moe_route_rule* rule,
                          size_t ws_bytes, void* stream) {
     if (!p) return MOE_ERR_ARG;
     RouteLogitsLaunch rl{};
-    if (rule) {
-        int rc = check_shape(p->T, p->D, p->E, p->K, p->f, p->f_s);
-        if (rc) return rc;
-        if ((rc = check_rule(rule, p->E, p->K))) return rc;
-        if (p->score_mode || p->select_bias || (p->flags & MOE_FLAG_BF16_WEIGHTS)) return MOE_ERR_ARG;
-        rl = rule_launch(rule);
-    }
+    const int rc = rule ? check_layer_rule(p, rule) : MOE_OK;
+    if (rc) return rc;
+    if (rule) rl = rule_launch(rule);
     if (weights) return layer_int8(p, rule ? &rl : nullptr, weights, out, workspace, ws_bytes,
                                    as_stream(stream));
     return layer_forward(p, rule ? &rl : nullptr, out, workspace, ws_bytes, stream);
+}
+
+int moe_layer_plan_ex(const moe_layer_params* p, const moe_route_rule* rule, unsigned* step_mask,
+                      int* launches) {
+    if (!p) return MOE_ERR_ARG;
+    if (!rule) return moe_layer_plan(p, step_mask, launches);
+    const int rc = check_layer_rule(p, rule);
+    if (rc) return rc;
+    const RouteLogitsLaunch rl = rule_launch(rule);
+    return layer_plan(p, &rl, step_mask, launches);
 }
 
 }  // extern "C"

@@ -518,9 +518,8 @@ int moe::layer_forward(const moe_layer_params* p, const RouteLogitsLaunch* rule,
     return mark(MOE_EV_END) ? MOE_OK : MOE_ERR_CUDA;
 }
 
-extern "C" {
-
-int moe_layer_plan(const moe_layer_params* p, unsigned* step_mask, int* launches) {
+int moe::layer_plan(const moe_layer_params* p, const RouteLogitsLaunch* rule, unsigned* step_mask,
+                    int* launches) {
     int rc = check_layer(p, nullptr);
     if (rc) return rc;
     unsigned mask = 0;
@@ -528,8 +527,10 @@ int moe_layer_plan(const moe_layer_params* p, unsigned* step_mask, int* launches
     if (p->T > 0) {
         const int sms = num_sms_current();
         // nothing is dereferenced: the plan only needs the workspace's layout
-        const LayerPlan q = plan_layer(p, nullptr, reinterpret_cast<void*>(kAlign), sms);
-        const int nr = q.tc_router ? 2 : 1;
+        const LayerPlan q = plan_layer(p, nullptr, reinterpret_cast<void*>(kAlign), sms, rule);
+        // logits and selection, in one kernel on the CUDA cores unless a rule selects; the shared
+        // gate is then one more
+        const int nr = rule ? 2 + (q.shared_launches ? 1 : 0) : q.tc_router ? 2 : 1;
         const int np = permute_chunks(static_cast<long long>(p->T) * p->K) > 1 ? 2 : 1;
         const int nu = grouped_gemm_launches(q.up, sms), nd = grouped_gemm_launches(q.dn, sms);
         const int ns = q.shared_launches ? grouped_gemm_launches(q.su, sms) + grouped_gemm_launches(q.sd, sms) : 0;
@@ -543,6 +544,12 @@ int moe_layer_plan(const moe_layer_params* p, unsigned* step_mask, int* launches
     if (step_mask) *step_mask = mask;
     if (launches) *launches = n;
     return MOE_OK;
+}
+
+extern "C" {
+
+int moe_layer_plan(const moe_layer_params* p, unsigned* step_mask, int* launches) {
+    return layer_plan(p, nullptr, step_mask, launches);
 }
 
 int moe_ep_dispatch_rows(const moe_bf16* x, const int32_t* sorted_token, int rows, int D,
