@@ -1,0 +1,38 @@
+"""Ways of calling the binding's functions, on the CPU as far as their own checks."""
+import pytest
+import torch
+
+import top_routing_grouped_03_b200 as moe
+from top_routing_grouped_03_b200 import build as moe_build
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    moe_build.build()
+    return moe.lib()
+
+
+X = torch.zeros(4, 64, dtype=torch.bfloat16)
+W, S = torch.zeros(8, 64, dtype=torch.int8), torch.zeros(8)
+NAMED = [(moe.route_logits, dict(logits=torch.zeros(4, 64), K=4)),
+         (moe.quantize_rows, dict(x=X)),
+         (moe.int8_matmul, dict(xq=W, x_scale=S, wq=W, w_scale=S)),
+         (moe.int8_linear, dict(x=X, wq=W, w_scale=S)),
+         (moe.experts_int8, dict(xq=W, x_scale=S, topk_w=S, perm={}, w_gate_up=W, gate_up_scale=S, w_down=W,
+                                 down_scale=S))]
+
+
+@pytest.mark.parametrize("call,kw", NAMED, ids=lambda v: getattr(v, "__name__", ""))
+def test_every_argument_by_name(call, kw):
+    """(Host tensors: refused as such, also with a stream, by the names the signature has.)"""
+    for extra in ({}, dict(stream=None)):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call(**kw, **extra)
+    first = next(iter(kw))
+    rest = {k: v for k, v in kw.items() if k != first}
+    with pytest.raises(TypeError, match=first):
+        call(**rest)
+    with pytest.raises(TypeError, match=first):
+        call(kw[first], **kw)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        call(kw[first], **rest)

@@ -320,19 +320,24 @@ _get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRa
 def _on_device_of(fn):
     """Runs fn with its first argument's device current and its ``stream`` (default: that
     device's current stream) as the current one, so that what fn allocates belongs to it."""
+    name = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
+        first = args[0] if args else kw.get(name)
+        if first is None or (args and name in kw):
+            return fn(*args, **kw)  # says what is wrong
         index = first.get_device()
         if index < 0:
             raise ValueError("expected a CUDA tensor")
         if stream is None and index == _get_device():
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
         if stream is None:
             stream = torch.cuda.current_stream(index)
         if stream.device != first.device:
             raise ValueError(f"stream on {stream.device}, tensors on {first.device}")
         with torch.cuda.stream(stream):
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
     return call
 
 
