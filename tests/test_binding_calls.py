@@ -1,7 +1,11 @@
 """Ways of calling the binding's functions, on the CPU as far as their own checks."""
+import subprocess
+import sys
+
 import pytest
 import torch
 
+from conftest import ROOT
 import top_routing_grouped_03_b200 as moe
 from top_routing_grouped_03_b200 import build as moe_build
 
@@ -36,3 +40,26 @@ def test_every_argument_by_name(call, kw):
         call(kw[first], **kw)
     with pytest.raises(ValueError, match="CUDA tensor"):
         call(kw[first], **rest)
+
+
+WITHOUT_PRIVATE_NAMES = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import top_routing_grouped_03_b200 as moe
+try:
+    moe.quantize_rows(torch.zeros(4, 64, dtype=torch.bfloat16))
+except ValueError as e:
+    print("refused:", e)
+assert moe._get_device is torch.cuda.current_device
+torch.cuda.current_stream = lambda index: type("Stream", (), dict(cuda_stream=70 + index))
+assert moe._raw_stream(3) == 73
+"""
+
+
+def test_a_torch_without_the_private_names_still_imports():
+    """As a CPU build of torch is: the package imports, and its calls raise."""
+    r = subprocess.run([sys.executable, "-c", WITHOUT_PRIVATE_NAMES], cwd=ROOT, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "refused: expected a CUDA tensor" in r.stdout, r.stderr

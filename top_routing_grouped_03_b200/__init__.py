@@ -314,7 +314,11 @@ def _need(ok: bool, what: str):
 
 
 _empty = torch.empty_strided  # (the call that costs the host least)
-_get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# torch's own, without the objects around them, which small calls notice; a torch without them, as
+# one built for the CPU, takes the public ones
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _on_device_of(fn):
