@@ -63,3 +63,32 @@ def test_a_torch_without_the_private_names_still_imports():
     r = subprocess.run([sys.executable, "-c", WITHOUT_PRIVATE_NAMES], cwd=ROOT, capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0 and "refused: expected a CUDA tensor" in r.stdout, r.stderr
+
+
+def test_sizes_past_32_bits_are_refused():
+    """Not cut to their low 32 bits on the way to the C ABI."""
+    for bad in (2 ** 31, 2 ** 32 + 8, 2 ** 40):
+        for sizes in ((bad,), (4, bad), (bad, 0), (-1, bad)):
+            with pytest.raises(moe.MoEError) as e:
+                moe._sizes("call", *sizes)
+            assert e.value.code == -2
+    moe._sizes("call", 0, 1, 2 ** 31 - 1)
+    moe._sizes("call", -1, 4)  # (negative sizes are the library's to refuse)
+    for kw in (dict(n_group=2 ** 32 + 2), dict(topk_group=2 ** 32 + 1), dict(group_top=2 ** 32 + 1)):
+        with pytest.raises(moe.MoEError):
+            moe.route_rule(64, 2, **kw)
+
+
+@pytest.mark.gpu
+def test_tensors_past_32_bit_rows_are_refused():
+    rows = 2 ** 32 + 1
+    before = moe.launch_count()
+    logits = torch.empty((rows, 1), dtype=torch.bfloat16, device="cuda")  # 8 GiB, never written
+    with pytest.raises(moe.MoEError):
+        moe.route_logits(logits, 1)
+    del logits
+    w = torch.empty((2 ** 28 + 8, 16), dtype=torch.int8, device="cuda")  # 2^32 values, in rows of 16
+    x, s = torch.zeros(1, 16, dtype=torch.bfloat16, device="cuda"), torch.ones(1, device="cuda")
+    with pytest.raises(moe.MoEError):
+        moe.int8_linear(x, w, s.expand(2 ** 28 + 8).contiguous())  # (more rows than the library takes)
+    assert moe.launch_count() == before

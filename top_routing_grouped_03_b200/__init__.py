@@ -356,6 +356,12 @@ def _q(t, dtype, index):
     return _p(t, dtype)  # says what is wrong
 
 
+def _sizes(what, *sizes):
+    """The C ABI takes these as 32-bit ints, and ctypes would hand over their low 32 bits."""
+    if max(sizes) > 0x7fffffff:
+        raise MoEError(-2, f"{what} (a size of 2^31 or more)")
+
+
 def route_rule(E, K, score="softmax", select_bias=None, n_group=1, topk_group=1, group_top=None,
                renorm=True, scale=1.0) -> RouteRule:
     """A moe_route_rule for routers of E experts (and K of them a token, which the groups that
@@ -363,6 +369,7 @@ def route_rule(E, K, score="softmax", select_bias=None, n_group=1, topk_group=1,
     best keys) and 1 without."""
     if select_bias is not None:
         _need(select_bias.shape == (E,), "route_rule (select_bias must be [E])")
+    _sizes("route_rule", E, K, n_group, topk_group, 1 if group_top is None else group_top)
     if n_group > 0 and E % n_group == 0:
         _need(K <= topk_group * (E // n_group), "route_rule (K experts in the groups that stay)")
     if group_top is None:
@@ -393,6 +400,7 @@ def route_logits(logits, K, score="softmax", select_bias=None, n_group=1, topk_g
     _need(logits.dim() == 2, "route_logits (logits must be [T, E])")
     T, E = logits.shape
     dev = logits.get_device()
+    _sizes("route_logits", T, E, K, n_group, topk_group, 1 if group_top is None else group_top)
     kind = 0 if logits.dtype is F32 else 1
     if select_bias is not None:
         _need(select_bias.numel() == E, "route_logits (select_bias must be [E])")
@@ -419,6 +427,7 @@ def quantize_rows(x):
     p = _q(x, BF16, dev)
     shape, stride, device = x.shape, x.stride(), x.device  # (x is contiguous)
     cols = shape[-1]
+    _sizes("quantize_rows", cols)
     q = _empty(shape, stride, dtype=I8, device=device)
     if len(shape) == 2:
         scale = _empty((shape[0],), (1,), dtype=F32, device=device)
@@ -447,6 +456,7 @@ def int8_matmul(xq, x_scale, wq, w_scale, workspace=None, out=None):
     _need(xq.dim() == 2 and wq.dim() == 2 and xq.shape[1] == wq.shape[1],
           "int8_matmul (xq must be [T, K], wq [N, K])")
     (T, K), N, dev = xq.shape, wq.shape[0], xq.get_device()
+    _sizes("int8_matmul", T, K, N)
     _need(x_scale.shape == (T,) and w_scale.shape == (N,), "int8_matmul (one scale per row)")
     a = _q(xq, I8, dev), _q(x_scale, F32, dev), _q(wq, I8, dev), _q(w_scale, F32, dev)
     out, ws, n = _int8_buffers(xq, T, N, K, out, workspace)
@@ -462,6 +472,7 @@ def int8_linear(x, wq, w_scale, workspace=None, out=None):
     _need(x.dim() == 2 and wq.dim() == 2 and x.shape[1] == wq.shape[1],
           "int8_linear (x must be [T, K], wq [N, K])")
     (T, K), N, dev = x.shape, wq.shape[0], x.get_device()
+    _sizes("int8_linear", T, K, N)
     _need(w_scale.shape == (N,), "int8_linear (one scale per weight row)")
     a = _q(x, BF16, dev), _q(wq, I8, dev), _q(w_scale, F32, dev)
     out, ws, n = _int8_buffers(x, T, N, K, out, workspace)
@@ -490,6 +501,7 @@ def experts_int8(xq, x_scale, topk_w, perm, w_gate_up, gate_up_scale, w_down, do
     offsets, token, weight, row = (perm["offsets"], perm["sorted_token"], perm["sorted_w"],
                                    perm["slot_to_row"])
     n = T * K
+    _sizes("experts_int8", T, D, E, K, f)
     _need(offsets.numel() == E + 1 and token.numel() == n and weight.numel() == n
           and row.numel() == n, "experts_int8 (perm of another routing)")
     _need((out is None or out.shape == (T, D)) and (residual is None or residual.shape == (T, D)),
