@@ -1,0 +1,69 @@
+"""A layer's workspace stays in place for as long as a captured graph, or work on another stream,
+uses it."""
+import weakref
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def make(moe, int8):
+    g = torch.Generator().manual_seed(3)
+
+    def r(*s):
+        return (torch.randn(*s, generator=g) / 16).bfloat16().cuda()
+
+    cls = moe.Int8MoELayer if int8 else moe.MoELayer
+    return cls(r(16, 256), r(16, 256, 256), r(16, 256, 128), 2, deterministic=True), r
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_a_captured_call_keeps_its_workspace(moe, int8):
+    layer, r = make(moe, int8)
+    x, big = r(24, 256), r(3000, 256)
+    want = layer(x)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = layer(x)
+    old = weakref.ref(layer._ws)
+    size = layer._ws.numel()
+    layer(big)
+    assert layer._ws is not old() and old() is not None
+    # nobody else gets the memory that replays write to
+    others = [torch.full((size,), 17, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    for _ in range(3):
+        y.zero_()
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and all(bool((o == 17).all()) for o in others)
+    # captured again, on the workspace of now: one more is kept, not one for every call
+    g2 = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g2):
+        layer(x)
+        layer(x)
+    assert len(layer._captured_ws) == 2
+    del g, g2
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_a_workspace_in_use_on_another_stream_is_not_handed_on(moe, int8):
+    layer, r = make(moe, int8)
+    x, big = r(2000, 256), r(4000, 256)
+    want = layer(x)
+    side = torch.cuda.Stream()
+    layer._ws = None
+    layer._ws_T = -1
+    ptr, size = layer.workspace(2000).data_ptr(), layer._ws.numel()
+    side.wait_stream(torch.cuda.current_stream())
+    ys = []
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # (some ms) the call below is still to come when the layer moves on
+    ys.append(layer(x, stream=side))
+    layer.workspace(4000)
+    held = torch.empty(size, dtype=torch.uint8, device="cuda")
+    assert held.data_ptr() != ptr
+    torch.cuda.synchronize()
+    assert torch.equal(ys[0], want)
+    assert torch.equal(layer(big)[:1].isfinite(), torch.ones(1, 256, dtype=torch.bool, device="cuda"))

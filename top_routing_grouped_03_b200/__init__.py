@@ -585,6 +585,9 @@ class MoELayer:
     """One MoE layer with resident weights and a reusable workspace.
 
     ``layer(x)`` runs moe_layer_forward on the current stream and returns y [T, D] bf16.
+    Calls share the layer's workspace, so they must not overlap on the GPU (one stream, or
+    ordered by events), replays of captured calls included.  A larger batch replaces the
+    workspace; the one that a captured call used stays with the layer.
     """
 
     def __init__(self, w_router, w_gate_up, w_down, K, logit_bias=None, w_shared_gate=None,
@@ -610,6 +613,7 @@ class MoELayer:
         self._int8 = None
         self._ws = None
         self._ws_T = -1
+        self._captured_ws = []
         self._copy_streams = None
 
     @classmethod
@@ -624,6 +628,16 @@ class MoELayer:
                                        self.w_router.device)
             self._ws_T = T
         return self._ws
+
+    def _hold(self, ws, stream):
+        """A graph that is being captured keeps the workspace's address, and work on another
+        stream than the one the workspace was allocated on may outlast it: neither may find the
+        memory in other hands once a larger batch has replaced the workspace."""
+        if torch.cuda.is_current_stream_capturing():
+            if not any(w is ws for w in self._captured_ws):
+                self._captured_ws.append(ws)
+        elif stream is not None:
+            ws.record_stream(stream)
 
     def params(self, x, topk_idx=None, topk_w=None, counts=None, events=None,
                residual=None) -> LayerParams:
@@ -648,6 +662,7 @@ class MoELayer:
         out = out if out is not None else torch.empty((T, self.D), dtype=torch.bfloat16,
                                                       device=x.device)
         ws = self.workspace(T)
+        self._hold(ws, stream)
         prm = self.params(x, topk_idx, topk_w, counts, step_events, residual)
         if self.rule is None and self._int8 is None:
             rc = lib().moe_layer_forward(ctypes.byref(prm), _p(out, BF16), _p(ws, U8), ws.numel(),
