@@ -468,7 +468,8 @@ def int8_matmul(xq, x_scale, wq, w_scale, workspace=None, out=None):
 @_on_device_of
 def int8_linear(x, wq, w_scale, workspace=None, out=None):
     """A linear layer in 8-bit integers: x [T, K] bf16 quantised per row, times wq [N, K] int8
-    with w_scale [N]; returns [T, N] bf16 (moe_int8_linear)."""
+    with w_scale [N]; returns [T, N] bf16 (moe_int8_linear).  A ``workspace`` of the caller's holds
+    the status word that read_device_status reads (a handful of tokens uses none)."""
     _need(x.dim() == 2 and wq.dim() == 2 and x.shape[1] == wq.shape[1],
           "int8_linear (x must be [T, K], wq [N, K])")
     (T, K), N, dev = x.shape, wq.shape[0], x.get_device()
@@ -488,7 +489,8 @@ def experts_int8(xq, x_scale, topk_w, perm, w_gate_up, gate_up_scale, w_down, do
     x_scale [T] (quantize_rows), weights w_gate_up [E, 2f, D] and w_down [E, D, f] int8 with
     gate_up_scale [E, 2f] and down_scale [E, D], for the routing weights topk_w [T, K] and
     ``perm`` = permute(...).  Returns out [T, D] bf16 (+ residual).  Rows of ``perm`` are trusted:
-    they must index the T tokens and the E experts."""
+    they must index the T tokens and the E experts.  A ``workspace`` of the caller's holds the
+    status word that read_device_status reads."""
     _need(xq.dim() == 2 and w_down.dim() == 3 and topk_w.dim() == 2,
           "experts_int8 (xq [T, D], topk_w [T, K], w_gate_up [E, 2f, D], w_down [E, D, f])")
     T, D = xq.shape

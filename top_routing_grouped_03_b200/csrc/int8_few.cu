@@ -16,8 +16,7 @@
 //     starts with gate_up and brings its weights into L2 until h is there.  (h quantised by
 //     every CTA of down for itself, as linear does with its tokens, took 8 us longer than the
 //     launch in between: 512 CTAs read the same 32 KB.)  Each (token, expert) row reads its
-//     weights for itself; at most kFewRows rows, so two tokens with a common expert at worst
-//     read it twice.
+//     weights for itself, from L2 where rows share an expert; see few_experts_ok.
 #include <algorithm>
 
 #include "quantize.cuh"
@@ -329,6 +328,12 @@ __global__ void __launch_bounds__(kThreads, kExpertCtas) few_down_kernel(Int8Few
 
 }  // namespace
 
+// Up to 8 tokens, as far as they fit in shared memory.  us here against the tiles with their rows'
+// launch, by tokens (weights from HBM): 1024 x 1024 1: 2.7/8.0, 8: 4.8/7.9; 4096 x 4096 1: 6.3/20.1,
+// 4: 10.1/19.7, 8: 15.9/18.6.  A token costs a dp4a for every four weights, so larger matrices cross
+// earlier: 4096 x 8192 4: 17.4/20.8, 5: 22.9/21.0, 8: 29.1/20.5; 14336 x 4096 4: 17.5/22.6, 5:
+// 22.5/22.1, 8: 31.3/21.4.  The limit does not follow them: callers rely on it for calls without a
+// workspace.
 bool few_linear_ok(int T, int K) {
     return T <= 8 && static_cast<long long>(T) * ((K + 15) & ~15) <= 65536;
 }
@@ -343,6 +348,9 @@ cudaError_t launch_few_linear(const bf16* x, const int8_t* xq, const float* x_sc
                     : launch_linear<8>(a, num_sms, s);
 }
 
+// Up to 16 rows.  us here against weights on M, 128 experts of D 2048, f 512 and of 4096, 1024: 8 rows of
+// one token 12.4/24.2 and 23.9/35.4; 16 rows of 2 tokens 18.1/26.6 and 41.2/48.8; 16 tokens with an
+// expert each 19.0/26.6 and 49.9/48.9, all with the same expert 17.3/24.6 and 33.5/32.8.
 bool few_experts_ok(int T, int D, int K, int f) {
     const long long rows = static_cast<long long>(T) * K;
     return rows <= kFewRows && static_cast<long long>(T) * D <= 65536 && rows * f <= 65536;
