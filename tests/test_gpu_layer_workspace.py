@@ -53,14 +53,16 @@ def test_a_workspace_in_use_on_another_stream_is_not_handed_on(moe, int8):
     x, big = r(2000, 256), r(4000, 256)
     want = layer(x)
     side = torch.cuda.Stream()
-    layer._ws = None
-    layer._ws_T = -1
-    ptr, size = layer.workspace(2000).data_ptr(), layer._ws.numel()
-    side.wait_stream(torch.cuda.current_stream())
+    ptr, size = layer._ws.data_ptr(), layer._ws.numel()
+    # memory for the larger workspace is at hand: taking it does not wait for the GPU
+    other, _ = make(moe, int8)
+    other.workspace(4000)
+    del other
+    torch.cuda.synchronize()
     ys = []
     with torch.cuda.stream(side):
-        torch.cuda._sleep(20_000_000)  # (some ms) the call below is still to come when the layer moves on
-    ys.append(layer(x, stream=side))
+        torch.cuda._sleep(500_000_000)  # (a quarter of a second) the call below is still to come when
+    ys.append(layer(x, stream=side))    # the layer moves on
     layer.workspace(4000)
     held = torch.empty(size, dtype=torch.uint8, device="cuda")
     assert held.data_ptr() != ptr

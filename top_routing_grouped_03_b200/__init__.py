@@ -319,6 +319,7 @@ _empty = torch.empty_strided  # (the call that costs the host least)
 _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 
 
 def _on_device_of(fn):
@@ -328,8 +329,11 @@ def _on_device_of(fn):
 
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
-        first = args[0] if args else kw.get(name)
-        if first is None or (args and name in kw):
+        if args and name not in kw:
+            first = args[0]
+        elif name in kw and not args:
+            first = kw[name]
+        else:
             return fn(*args, **kw)  # says what is wrong
         index = first.get_device()
         if index < 0:
@@ -357,7 +361,8 @@ def _q(t, dtype, index):
 
 
 def _sizes(what, *sizes):
-    """The C ABI takes these as 32-bit ints, and ctypes would hand over their low 32 bits."""
+    """The C ABI takes these as 32-bit ints, and ctypes would hand over their low 32 bits.  (Calls
+    that small batches make look at the bits of all first.)"""
     if max(sizes) > 0x7fffffff:
         raise MoEError(-2, f"{what} (a size of 2^31 or more)")
 
@@ -400,7 +405,8 @@ def route_logits(logits, K, score="softmax", select_bias=None, n_group=1, topk_g
     _need(logits.dim() == 2, "route_logits (logits must be [T, E])")
     T, E = logits.shape
     dev = logits.get_device()
-    _sizes("route_logits", T, E, K, n_group, topk_group, 1 if group_top is None else group_top)
+    if (T | E | K | n_group | topk_group) >> 31:
+        _sizes("route_logits", T, E, K, n_group, topk_group)
     kind = 0 if logits.dtype is F32 else 1
     if select_bias is not None:
         _need(select_bias.numel() == E, "route_logits (select_bias must be [E])")
@@ -427,7 +433,8 @@ def quantize_rows(x):
     p = _q(x, BF16, dev)
     shape, stride, device = x.shape, x.stride(), x.device  # (x is contiguous)
     cols = shape[-1]
-    _sizes("quantize_rows", cols)
+    if cols >> 31:
+        _sizes("quantize_rows", cols)
     q = _empty(shape, stride, dtype=I8, device=device)
     if len(shape) == 2:
         scale = _empty((shape[0],), (1,), dtype=F32, device=device)
@@ -456,7 +463,8 @@ def int8_matmul(xq, x_scale, wq, w_scale, workspace=None, out=None):
     _need(xq.dim() == 2 and wq.dim() == 2 and xq.shape[1] == wq.shape[1],
           "int8_matmul (xq must be [T, K], wq [N, K])")
     (T, K), N, dev = xq.shape, wq.shape[0], xq.get_device()
-    _sizes("int8_matmul", T, K, N)
+    if (T | K | N) >> 31:
+        _sizes("int8_matmul", T, K, N)
     _need(x_scale.shape == (T,) and w_scale.shape == (N,), "int8_matmul (one scale per row)")
     a = _q(xq, I8, dev), _q(x_scale, F32, dev), _q(wq, I8, dev), _q(w_scale, F32, dev)
     out, ws, n = _int8_buffers(xq, T, N, K, out, workspace)
@@ -473,7 +481,8 @@ def int8_linear(x, wq, w_scale, workspace=None, out=None):
     _need(x.dim() == 2 and wq.dim() == 2 and x.shape[1] == wq.shape[1],
           "int8_linear (x must be [T, K], wq [N, K])")
     (T, K), N, dev = x.shape, wq.shape[0], x.get_device()
-    _sizes("int8_linear", T, K, N)
+    if (T | K | N) >> 31:
+        _sizes("int8_linear", T, K, N)
     _need(w_scale.shape == (N,), "int8_linear (one scale per weight row)")
     a = _q(x, BF16, dev), _q(wq, I8, dev), _q(w_scale, F32, dev)
     out, ws, n = _int8_buffers(x, T, N, K, out, workspace)
@@ -503,7 +512,8 @@ def experts_int8(xq, x_scale, topk_w, perm, w_gate_up, gate_up_scale, w_down, do
     offsets, token, weight, row = (perm["offsets"], perm["sorted_token"], perm["sorted_w"],
                                    perm["slot_to_row"])
     n = T * K
-    _sizes("experts_int8", T, D, E, K, f)
+    if (T | D | E | K | f) >> 31:
+        _sizes("experts_int8", T, D, E, K, f)
     _need(offsets.numel() == E + 1 and token.numel() == n and weight.numel() == n
           and row.numel() == n, "experts_int8 (perm of another routing)")
     _need((out is None or out.shape == (T, D)) and (residual is None or residual.shape == (T, D)),
@@ -635,10 +645,10 @@ class MoELayer:
         """A graph that is being captured keeps the workspace's address, and work on another
         stream than the one the workspace was allocated on may outlast it: neither may find the
         memory in other hands once a larger batch has replaced the workspace."""
-        if torch.cuda.is_current_stream_capturing():
+        if _capturing():
             if not any(w is ws for w in self._captured_ws):
                 self._captured_ws.append(ws)
-        elif stream is not None:
+        else:
             ws.record_stream(stream)
 
     def params(self, x, topk_idx=None, topk_w=None, counts=None, events=None,
@@ -660,11 +670,13 @@ class MoELayer:
         T = x.shape[0]
         if x.shape[1] != self.D:
             raise MoEError(-1, "moe_layer_forward (x has the wrong width)")
-        _check_rule(self.rule, self.E, x)
+        if self.rule is not None:
+            _check_rule(self.rule, self.E, x)
         out = out if out is not None else torch.empty((T, self.D), dtype=torch.bfloat16,
                                                       device=x.device)
         ws = self.workspace(T)
-        self._hold(ws, stream)
+        if stream is not None or _capturing():
+            self._hold(ws, stream)
         prm = self.params(x, topk_idx, topk_w, counts, step_events, residual)
         if self.rule is None and self._int8 is None:
             rc = lib().moe_layer_forward(ctypes.byref(prm), _p(out, BF16), _p(ws, U8), ws.numel(),
