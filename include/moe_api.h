@@ -406,7 +406,8 @@ MOE_API int moe_read_device_status(void* workspace, void* stream);
  *   I     = TopK(key, K) inside those groups, by descending key, ties to the lower index
  *   w_e   = scale * s_e / (renorm ? sum_{j in I} s_j : 1)
  * The order is that of the real numbers key_e: fp32 values that are too close to tell are
- * compared again in fp64.  A logit of -inf or NaN takes its expert out for that token (so
+ * compared again in fp64 (where fp64 cannot tell either, as between saturated sigmoids with a bias,
+ * the lower index comes first).  A logit of -inf or NaN takes its expert out for that token (so
  * does a bias of -inf or NaN for all tokens): it adds to no group score, is chosen only when
  * fewer than K others are left, and has weight 0.  A logit of +inf counts as the largest
  * finite number.  n_group <= 32 divides E, 1 <= topk_group <= n_group, and

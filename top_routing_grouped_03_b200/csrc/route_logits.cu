@@ -333,13 +333,14 @@ __device__ __forceinline__ unsigned pick_groups(const RouteLogitsLaunch& a, Judg
     return allowed;
 }
 
-// Weights from differences of logits, for scores whose sum (nearly) underflows: there
-// sigma(r) = e^r to fp32 accuracy.
-__device__ __noinline__ float far_weight(float l) {
-    float best = l;
-    for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(kAll, best, o));
+// Renormalised weights of the slots' logits l by their differences: those of a softmax, and of
+// sigmoids that are all below 4e-8, where sigma(r) = e^r to fp32 accuracy.  However small the scores
+// are, the ratios keep their digits.
+__device__ __forceinline__ float weight_by_difference(float l) {
+    const float best = unordered(__reduce_max_sync(kAll, ordered(l)));
     const float s = l > -INFINITY ? expf(l - best) : 0.f;
     float sum = s;
+#pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
     return sum > 0.f ? s / sum : 0.f;
 }
@@ -511,20 +512,22 @@ __device__ __forceinline__ void route_token(const RouteLogitsLaunch& a, long lon
         my_e = exact_topk<T>(a, token, reinterpret_cast<double*>(sm), allowed, lane);
         if (lane < K) l = token_logit<T>(a, token, my_e);
     }
-    // weights: the selected scores, in the lanes of their slots
+    // weights: the selected scores, in the lanes of their slots (an expert that is out: 0)
+    if (lane < K && a.select_bias && !(__ldg(a.select_bias + my_e) > -INFINITY)) l = -INFINITY;
     float w = 0.f;
-    if (lane < K) {
-        w = SIGMOID ? 1.f / (1.f + expf(-l)) : expf(l - m) / z;
-        if (!(l > -INFINITY) || (a.select_bias && !(w + __ldg(a.select_bias + my_e) > -INFINITY))) {
-            l = -INFINITY;
-            w = 0.f;
-        }
-    }
-    if (a.renorm) {
-        float sum = w;
+    if (!SIGMOID && a.renorm) {
+        w = weight_by_difference(l);
+    } else if (!SIGMOID) {
+        if (l > -INFINITY) w = expf(l - m) / z;
+    } else {
+        const float e = expf(-fabsf(l));  // at most 1: no overflow, and subnormal scores survive
+        if (l > -INFINITY) w = (l < 0.f ? e : 1.f) / (1.f + e);
+        if (a.renorm) {
+            float sum = w;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-        w = sum < 1e-30f ? far_weight(l) : w / sum;
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+            w = sum < 4e-8f ? weight_by_difference(l) : w / sum;
+        }
     }
     if (lane < K) {
         a.topk_idx[token * K + lane] = my_e;
