@@ -64,3 +64,13 @@ def test_a_bias_on_another_device_is_refused():
         moe.route(x, w_router, 2, rule=rule)
     with pytest.raises(ValueError, match="cuda:1"):
         moe.MoELayer(w_router, gu, dn, 2, rule=rule)
+
+
+def test_a_workspace_off_its_alignment_is_refused():
+    import ctypes
+    p = ctypes.c_void_p
+    rule = moe.route_rule(128, 2)
+    for T in (4, 300):  # CUDA-core and tensor-core logits
+        for off, code in ((4, -3), (8, -3)):
+            assert moe.lib().moe_route_rule_ex(p(0x10000), p(0x10000), None, None, T, 256, 128, 2, rule, p(0x10000),
+                                               p(0x10000), p(0x10000), None, p(0x10000 + off), 1 << 40, None) == code

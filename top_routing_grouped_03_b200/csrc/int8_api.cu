@@ -477,6 +477,7 @@ int moe_route_rule_ex(const moe_bf16* x, const moe_bf16* w_router, const float* 
     if (T > 0 && (!x || !topk_idx || !topk_w || (w_shared_gate && !shared_gate))) return MOE_ERR_ARG;
     if (!aligned16(x) || !aligned16(w_router) || !aligned16(w_shared_gate)) return MOE_ERR_ALIGN;
     if (!workspace || ws_bytes < moe_workspace_size(T, D, E, K, 128, 0)) return MOE_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MOE_ERR_ALIGN;  // the logits are stored in vectors
     cudaStream_t s = as_stream(stream);
     const RouteLogitsLaunch rl = rule_launch(rule);
     if (T == 0)
