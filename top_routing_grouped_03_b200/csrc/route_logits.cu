@@ -26,9 +26,9 @@
 // by warp-wide maxima; others go through shared memory.
 //
 // 16381 x 256 fp32 logits, K = 8, 3 of 8 groups by their best key: 20.7 us (17 MB, 2.6 us of memory
-// traffic; 34.8 with K rounds), bound by instruction issue (800 instructions a token, 2.4 of 4
+// traffic; 34.8 with K rounds), bound by instruction issue (800 instructions a token, 2.3 of 4
 // slots used).  4096 x 512, K = 10, 5 of 16 groups by two keys, bias: 20.2 us (58.9 with K rounds and
-// every doubtful token decided in fp64 from all of its keys), a chain of latencies (1.2 of 4 slots,
+// every doubtful token decided in fp64 from all of its keys), a chain of latencies (1.1 of 4 slots,
 // 39% of the warps).  One token 4.9 us.  Groups of 20, 32, 40 and 64 experts and none, the same rules on
 // other logits: 16381 x 240 or 256: 26.6, 20.5, 26.0, 24.7, 18.4 us; 4096 x 480 or 512: 19.0, 18.6,
 // 19.4, 19.8, 15.6.
