@@ -297,7 +297,7 @@ const char* moe_status_string(int status) {
     }
 }
 
-int moe_version(void) { return 110; }
+int moe_version(void) { return 111; }
 
 unsigned long long moe_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 
