@@ -1,5 +1,4 @@
-"""A layer's workspace stays in place for as long as a captured graph, or work on another stream,
-uses it."""
+"""A workspace stays in place for as long as a captured graph, or work on another stream, uses it."""
 import weakref
 
 import pytest
@@ -69,3 +68,33 @@ def test_a_workspace_in_use_on_another_stream_is_not_handed_on(moe, int8):
     torch.cuda.synchronize()
     assert torch.equal(ys[0], want)
     assert torch.equal(layer(big)[:1].isfinite(), torch.ones(1, 256, dtype=torch.bool, device="cuda"))
+
+
+@pytest.mark.parametrize("ruled", [False, True])
+def test_a_call_of_its_own_workspace_on_another_stream(moe, ruled, monkeypatch):
+    """The workspaces that route and permute allocate for one call, dropped before it has run."""
+    g = torch.Generator().manual_seed(4)
+    x = torch.randn(2000, 256, generator=g).bfloat16().cuda()
+    w = torch.randn(64, 256, generator=g).bfloat16().cuda()
+    rule = moe.route_rule(64, 4, n_group=4, topk_group=2) if ruled else None
+    want = moe.route(x, w, 4, rule=rule)
+    perm = moe.permute(want[0], want[1], want[2], 64)
+    lent, alloc = [], moe.alloc_workspace
+
+    def spy(*a, **k):
+        ws = alloc(*a, **k)
+        lent.append((ws.data_ptr(), ws.numel()))
+        return ws
+
+    monkeypatch.setattr(moe, "alloc_workspace", spy)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(500_000_000)
+    got = moe.route(x, w, 4, rule=rule, stream=side)
+    got_perm = moe.permute(got[0], got[1], got[2], 64, stream=side)
+    held = [torch.empty(n, dtype=torch.uint8, device="cuda") for _, n in lent]
+    assert len(lent) == 2 and not {h.data_ptr() for h in held} & {p for p, _ in lent}
+    torch.cuda.synchronize()
+    assert all(a is b is None or torch.equal(a, b) for a, b in zip(got, want))
+    assert all(torch.equal(got_perm[k], perm[k]) for k in perm)

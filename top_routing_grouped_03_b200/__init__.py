@@ -204,6 +204,13 @@ def alloc_workspace(T, D, E, K, f, f_s=0, device=None) -> torch.Tensor:
     return ws
 
 
+def _lend(workspace, stream):
+    """A workspace that is dropped when the call returns stays out of other hands until ``stream``, if
+    it is not the one the workspace was allocated on, has got past the call."""
+    if stream is not None:
+        workspace.record_stream(stream)
+
+
 def route(x, w_router, K, logit_bias=None, w_shared_gate=None, workspace=None, stream=None,
           score="softmax", select_bias=None, bf16_weights=False, rule=None):
     """Router step.  Returns (topk_idx [T,K] int32, topk_w [T,K] f32, expert_counts [E]
@@ -214,7 +221,10 @@ def route(x, w_router, K, logit_bias=None, w_shared_gate=None, workspace=None, s
     E = w_router.shape[0]
     dev = x.device
     _check_rule(rule, E, x)
-    ws = workspace if workspace is not None else alloc_workspace(T, D, E, K, 128, 0, dev)
+    ws = workspace
+    if ws is None:
+        ws = alloc_workspace(T, D, E, K, 128, 0, dev)
+        _lend(ws, stream)
     idx = torch.empty((T, K), dtype=torch.int32, device=dev)
     w = torch.empty((T, K), dtype=torch.float32, device=dev)
     counts = torch.empty((E,), dtype=torch.int32, device=dev)
@@ -273,6 +283,7 @@ def permute(topk_idx, topk_w, expert_counts, E, workspace=None, stream=None, cap
     s2r = torch.empty((T * K,), dtype=torch.int32, device=dev)
     if workspace is None and T > 0:
         workspace = alloc_workspace(T, 128, E, K, 128, 0, dev)
+        _lend(workspace, stream)
     cap = -1 if capacity is None else int(capacity)
     rc = lib().moe_permute_ex(_p(topk_idx, I32), _p(topk_w, F32), _p(expert_counts, I32), T, E,
                               K, cap, _p(off), _p(st), _p(sw), _p(s2r), _p(workspace, U8),
@@ -290,6 +301,7 @@ def grouped_swiglu(x, sorted_token, offsets, sorted_w, w_gate_up, w_down, rows,
     if workspace is None:
         Kr = max(1, -(-rows // max(T, 1)))
         workspace = alloc_workspace(max(T, 1), D, E, min(Kr, E, 16), f, 0, x.device)
+        _lend(workspace, stream)
     rc = lib().moe_grouped_swiglu(_p(x, BF16), _p(sorted_token, I32), _p(offsets, I32),
                                   _p(sorted_w, F32), _p(w_gate_up, BF16), _p(w_down, BF16), T,
                                   rows, D, E, f, _p(y_sorted, F32), _p(out_acc, F32),
